@@ -68,6 +68,16 @@ typedef enum {
     ARIA_FMT_F16 = 4    /* unquantised fp16 weights (the fp16 rung of the precision table) */
 } aria_format;
 
+/* Activation of a fused epilogue. GELU is z * Phi(z) (erf), GELU_TANH its
+ * tanh form 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))), SILU z / (1 + e^-z). */
+typedef enum {
+    ARIA_ACT_NONE = 0,
+    ARIA_ACT_RELU = 1,
+    ARIA_ACT_SILU = 2,
+    ARIA_ACT_GELU = 3,
+    ARIA_ACT_GELU_TANH = 4
+} aria_act;
+
 /* Human-readable name of a status code (static string). */
 const char *aria_status_string(aria_status s);
 
@@ -174,6 +184,95 @@ aria_status aria_qgemm_steer_dev(aria_format fmt, int group, int64_t M, int64_t 
                                  const void *X, const float *sx, const void *Wq,
                                  const void *scales, const void *bias, const float *steer_vec,
                                  const float *alpha_dev, void *Y, void *stream);
+
+/*
+ * aria_qgemm_act -- aria_qgemm with an activation and a residual add in its
+ * epilogue:
+ *   Y[m,n] = fp16( act(main[m,n] + bias[n]) + alpha * v[n] + R[m,n] )
+ * with `main` as for aria_qgemm. The steering add comes after the activation,
+ * on the residual stream ("Steering is real").
+ *   act        the activation; ARIA_ACT_NONE for none.
+ *   residual   device fp16 [M,N], or NULL. May be Y itself (the add is then in
+ *              place); any other overlap with Y is INVALID_ARG.
+ *   steer_vec, alpha   as for aria_qgemm; alpha_dev, if not NULL, a device
+ *              fp32 scalar (4-byte aligned) used instead of alpha, as in
+ *              aria_qgemm_steer_dev (ignored without steer_vec). A strength of
+ *              0 skips the add.
+ *   Every other argument and rule as for aria_qgemm. The epilogue is computed
+ *   in fp32 and rounded once, for W8A8 too: with act = NONE and no residual
+ *   the call is aria_qgemm, byte for byte; otherwise W8A8 results are within
+ *   2^-21 relative of the exact value before that one rounding.
+ * Deterministic; stream order as for aria_qgemm (the residual is touched only
+ * after the preceding kernel).
+ */
+aria_status aria_qgemm_act(aria_format fmt, int group, int64_t M, int64_t N, int64_t K,
+                           const void *X, const float *sx, const void *Wq, const void *scales,
+                           const void *bias, aria_act act, const void *residual,
+                           const float *steer_vec, float alpha, const float *alpha_dev, void *Y,
+                           void *stream);
+
+/*
+ * aria_qgemm_gated -- the gated half of a feed-forward block in one kernel:
+ *   g = main_g + bias_g,  u = main_u + bias_u,  H[m,n] = fp16( act(g) * u )
+ * with both projections' `main` as for aria_qgemm, from the same X.
+ *   Wg, scales_g, bias_g   the gate projection (as Wq, scales, bias of
+ *           aria_qgemm: [N,K] each); Wu, scales_u, bias_u the up projection,
+ *           of the same format and sizes.
+ *   act     applied to the gate (ARIA_ACT_NONE: the bare product).
+ *   H       device output fp16 [M,N].
+ *   G, U    device outputs fp16 [M,N] that receive g and u, each rounded once
+ *           (what aria_gated_bwd needs), or both NULL.
+ *   H, G and U must not overlap one another (INVALID_ARG) nor any input.
+ * g and u stay in fp32 up to the product; H is rounded once. Shape rules,
+ * errors and stream order as for aria_qgemm; both weights are loaded before
+ * the dependency wait. Deterministic; H does not depend on whether G and U
+ * are kept.
+ */
+aria_status aria_qgemm_gated(aria_format fmt, int group, int64_t M, int64_t N, int64_t K,
+                             const void *X, const float *sx, const void *Wg, const void *scales_g,
+                             const void *Wu, const void *scales_u, const void *bias_g,
+                             const void *bias_u, aria_act act, void *H, void *G, void *U,
+                             void *stream);
+
+/*
+ * aria_gated_bwd_workspace_size -- bytes of the workspace aria_gated_bwd needs
+ * for M tokens and N channels (two fp16 [M,N] and at most 64 fp32 [2N]).
+ * Errors: INVALID_ARG (NULL output, M or N outside [1, 2^31)).
+ */
+aria_status aria_gated_bwd_workspace_size(int64_t M, int64_t N, size_t *bytes);
+
+/*
+ * aria_gated_bwd -- gradients of aria_qgemm_gated on fp16 weights
+ * (ARIA_FMT_F16), from the pre-activations that it kept:
+ *   dG = dH * U * act'(G),        dU = dH * act(G)
+ *   dX = dG Wg + dU Wu            [M,K]
+ *   dWg = dG^T X,  dWu = dU^T X   [N,K]
+ *   dbg = sum_m dG,  dbu = sum_m dU   [N]
+ *   dH, G, U   device fp16 [M,N]; X device fp16 [M,K]; Wg, Wu device fp16 [N,K].
+ *   dX         device output, or NULL (then Wg and Wu may be NULL too).
+ *   dWg, dWu   device outputs, or both NULL (then X may be NULL).
+ *   dbg, dbu   device outputs fp16 [N], or both NULL.
+ *              At least one output is asked for (INVALID_ARG). Every output is
+ *              overwritten, not added to.
+ *   workspace  caller-owned device memory, 256-byte aligned, at least
+ *              aria_gated_bwd_workspace_size(M, N) bytes (INVALID_ARG
+ *              otherwise); its contents need no preparation and are
+ *              unspecified afterwards. Calls that share one must not overlap
+ *              on the GPU (one stream, or ordered by events).
+ *   Outputs and workspace share no byte with one another or with an input
+ *   (INVALID_ARG).
+ * The gradient of relu at 0 is 0. All sums are fp32 (in fixed order: the call
+ * is deterministic); dG and dU are rounded to fp16 as operands of the
+ * products, the bias gradients are summed before that rounding, and each
+ * output is rounded once. dH should be scaled so that dG, dU and the outputs
+ * stay within fp16's range, as fp16 training does anyway.
+ * Shape rules: M >= 1; N, K >= 16 and multiples of 16. Stream order: every
+ * input is read, and every output written, after the preceding kernel.
+ */
+aria_status aria_gated_bwd(aria_act act, int64_t M, int64_t N, int64_t K, const void *dH,
+                           const void *G, const void *U, const void *X, const void *Wg,
+                           const void *Wu, void *dX, void *dWg, void *dWu, void *dbg, void *dbu,
+                           void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * aria_w8a8_workspace_size -- bytes of the workspace aria_qgemm_w8a8_fused

@@ -29,9 +29,11 @@ ARIA_OK = 0
 STATUS = {0: "ARIA_OK", 1: "ARIA_ERR_INVALID_ARG", 2: "ARIA_ERR_UNSUPPORTED",
           3: "ARIA_ERR_MISALIGNED", 4: "ARIA_ERR_CUDA", 5: "ARIA_ERR_TIMEOUT"}
 FORMATS = {"q8": 1, "q4": 2, "w8a8": 3, "f16": 4}
+ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 API = ("aria_status_string", "aria_last_error_message", "aria_qpack_size", "aria_qpack",
        "aria_act_quant", "aria_qgemm", "aria_qgemm_steer_dev", "aria_w8a8_workspace_size",
        "aria_qgemm_w8a8_fused", "aria_qgemm_w8a8_fused_noalloc", "aria_qgemm_s32",
+       "aria_qgemm_act", "aria_qgemm_gated", "aria_gated_bwd_workspace_size", "aria_gated_bwd",
        "aria_selftest_bounded_wait", "aria_device_status")
 
 
@@ -66,6 +68,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                    ctypes.c_size_t, P], I),
         "aria_qgemm_w8a8_fused_noalloc": ([I64, I64, I64, P, P, P, P, P, ctypes.c_float, P, P, P], I),
         "aria_qgemm_s32": ([I64, I64, I64, P, P, P, P], I),
+        "aria_qgemm_act": ([I, I, I64, I64, I64, P, P, P, P, P, I, P, P, ctypes.c_float, P, P, P], I),
+        "aria_qgemm_gated": ([I, I, I64, I64, I64, P, P, P, P, P, P, P, P, I, P, P, P, P], I),
+        "aria_gated_bwd_workspace_size": ([I64, I64, P], I),
+        "aria_gated_bwd": ([I, I64, I64, I64, P, P, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P], I),
         "aria_selftest_bounded_wait": ([I64, I64, I64, P, P, P, P, P, ctypes.c_uint32, P], I),
         "aria_device_status": ([P], I),
     }
@@ -358,6 +364,220 @@ def qgemm_s32(Xq: torch.Tensor, Wq: torch.Tensor, out=None, stream=None):
                                              _dev(Wq, "Wq", torch.int8), _dev(C, "out", torch.int32),
                                              _stream(stream)))
     return C
+
+
+# --------------------------------------------------- feed-forward operators --
+
+def _act(act: str) -> int:
+    if act not in ACTS:
+        raise ValueError(f"unknown activation {act!r}: one of {', '.join(ACTS)}")
+    return ACTS[act]
+
+
+def _arg(t, name: str, shape: tuple, dtype, dev):
+    """Check one argument (None passes as NULL) and return its device pointer."""
+    if t is None:
+        return None
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, X on {dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _weight_args(fmt: str, W, scales, sfx: str, N: int, K: int, dev):
+    """Pointers of one packed weight [N,K] of the given format and its scales."""
+    if fmt == "f16":
+        if scales is not None:
+            raise ValueError("f16 weights take no scales")
+        return _arg(W, "W" + sfx, (N, K), torch.float16, dev), None
+    if scales is None:
+        raise ValueError(f"{fmt} needs scales")
+    if fmt == "q4":
+        if K % 32:
+            raise ValueError("q4 needs K % 32 == 0")
+        return (_arg(W, "W" + sfx, (N, K // 2), torch.uint8, dev),
+                _arg(scales, "scales" + sfx, (N, K // 32), torch.float16, dev))
+    return (_arg(W, "W" + sfx, (N, K), torch.int8, dev),
+            _arg(scales, "scales" + sfx, (N,), torch.float32, dev))
+
+
+def _x_args(fmt: str, X, W, sx):
+    """Sizes and pointers of the activations: (M, N, K, X, sx)."""
+    if fmt not in FORMATS:
+        raise ValueError(f"unknown format {fmt!r}")
+    if X.dim() != 2 or W.dim() != 2:
+        raise ValueError("X and the weights must be 2-D")
+    if not X.is_cuda:
+        raise ValueError("X must be a CUDA tensor (no CPU path exists)")
+    M, K = X.shape
+    w8a8 = fmt == "w8a8"
+    if w8a8 != (sx is not None):
+        raise ValueError("w8a8 needs sx" if w8a8 else "sx is for w8a8 only")
+    return (M, W.shape[0], K, _arg(X, "X", (M, K), torch.int8 if w8a8 else torch.float16, X.device),
+            _arg(sx, "sx", (M,), torch.float32, X.device))
+
+
+@contextlib.contextmanager
+def _running_on(dev, stream):
+    """Device and stream of one call: yields the stream's handle. With a stream
+    of the caller's, tensors that the call allocates come from that stream's
+    pool, so the memory is not still in use by work on another one."""
+    with torch.cuda.device(dev):
+        if stream is None:
+            yield torch.cuda.current_stream().cuda_stream
+        else:
+            s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(
+                _stream(stream), device=dev)
+            with torch.cuda.stream(s):
+                yield s.cuda_stream
+
+
+def qgemm_act(fmt: str, X: torch.Tensor, Wq: torch.Tensor, scales, sx=None, bias=None, act: str = "none",
+              residual=None, steer_vec=None, alpha: float = 0.0, group=None, out=None, stream=None,
+              alpha_dev=None):
+    """Y [M,N] fp16 = act(X . dequant(W)^T + bias) + alpha*v + residual, in one
+    kernel (include/aria_q.h, aria_qgemm_act).
+
+    Formats and arguments as for qgemm; ``act`` is one of ACTS; ``residual``
+    fp16 [M,N] may be ``out`` itself. With ``alpha_dev`` the strength is read
+    from device memory and ``alpha`` is ignored."""
+    M, N, K, px, psx = _x_args(fmt, X, Wq, sx)
+    dev = X.device
+    pw, ps = _weight_args(fmt, Wq, scales, "", N, K, dev)
+    pb = _arg(bias, "bias", (N,), torch.float16, dev)
+    pr = _arg(residual, "residual", (M, N), torch.float16, dev)
+    pv = _arg(steer_vec, "steer_vec", (N,), torch.float32, dev)
+    if alpha_dev is not None and alpha_dev.numel() != 1:
+        raise ValueError("alpha_dev must be one element")
+    pa = None if alpha_dev is None else _arg(alpha_dev, "alpha_dev", alpha_dev.shape, torch.float32, dev)
+    a, g, f = _act(act), _group(fmt, group), FORMATS[fmt]
+    po = _arg(out, "out", (M, N), torch.float16, dev)
+    lib = load_library()
+    if stream is None and dev.index == torch.cuda.current_device():
+        if out is None:
+            out = torch.empty(M, N, dtype=torch.float16, device=dev)
+            po = out.data_ptr()
+        st = lib.aria_qgemm_act(f, g, M, N, K, px, psx, pw, ps, pb, a, pr, pv, float(alpha), pa, po,
+                                torch.cuda.current_stream().cuda_stream)
+    else:
+        with _running_on(dev, stream) as raw:
+            if out is None:
+                out = torch.empty(M, N, dtype=torch.float16, device=dev)
+                po = out.data_ptr()
+            st = lib.aria_qgemm_act(f, g, M, N, K, px, psx, pw, ps, pb, a, pr, pv, float(alpha), pa, po, raw)
+    _check(st)
+    return out
+
+
+def qgemm_gated(fmt: str, X: torch.Tensor, Wg: torch.Tensor, scales_g, Wu: torch.Tensor, scales_u, sx=None,
+                bias_g=None, bias_u=None, act: str = "silu", group=None, out=None, save=None, stream=None):
+    """H [M,N] fp16 = act(g) * u with g = X . dequant(Wg)^T + bias_g and
+    u = X . dequant(Wu)^T + bias_u, in one kernel (include/aria_q.h,
+    aria_qgemm_gated).
+
+    Both weights have one format and shape (as Wq and scales of qgemm; "f16"
+    takes the fp16 weights and None for the scales). ``save`` = (G, U): fp16
+    [M,N] tensors that receive g and u, for gated_backward."""
+    M, N, K, px, psx = _x_args(fmt, X, Wg, sx)
+    dev = X.device
+    pg, psg = _weight_args(fmt, Wg, scales_g, "g", N, K, dev)
+    pu, psu = _weight_args(fmt, Wu, scales_u, "u", N, K, dev)
+    pbg = _arg(bias_g, "bias_g", (N,), torch.float16, dev)
+    pbu = _arg(bias_u, "bias_u", (N,), torch.float16, dev)
+    G, U = (None, None) if save is None else save
+    pG = _arg(G, "save[0]", (M, N), torch.float16, dev)
+    pU = _arg(U, "save[1]", (M, N), torch.float16, dev)
+    a, gr, f = _act(act), _group(fmt, group), FORMATS[fmt]
+    po = _arg(out, "out", (M, N), torch.float16, dev)
+    lib = load_library()
+    if stream is None and dev.index == torch.cuda.current_device():
+        if out is None:
+            out = torch.empty(M, N, dtype=torch.float16, device=dev)
+            po = out.data_ptr()
+        st = lib.aria_qgemm_gated(f, gr, M, N, K, px, psx, pg, psg, pu, psu, pbg, pbu, a, po, pG, pU,
+                                  torch.cuda.current_stream().cuda_stream)
+    else:
+        with _running_on(dev, stream) as raw:
+            if out is None:
+                out = torch.empty(M, N, dtype=torch.float16, device=dev)
+                po = out.data_ptr()
+            st = lib.aria_qgemm_gated(f, gr, M, N, K, px, psx, pg, psg, pu, psu, pbg, pbu, a, po, pG, pU, raw)
+    _check(st)
+    return out
+
+
+def gated_backward_workspace_size(M: int, N: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load_library().aria_gated_bwd_workspace_size(M, N, ctypes.byref(n)))
+    return n.value
+
+
+def gated_backward(dH: torch.Tensor, X, Wg, Wu, G: torch.Tensor, U: torch.Tensor, act: str = "silu",
+                   input_grad: bool = True, weight_grad: bool = True, bias_grad: bool = True, out=None,
+                   workspace=None, stream=None):
+    """Gradients of qgemm_gated("f16", ...) from the pre-activations it kept
+    (include/aria_q.h, aria_gated_bwd): (dX [M,K], dWg [N,K], dWu [N,K],
+    dbg [N], dbu [N]), fp16, None for those not asked for.
+
+    ``out``: a tuple of five tensors to write (None where nothing is asked
+    for). ``workspace``: a uint8 tensor of gated_backward_workspace_size(M, N)
+    bytes; calls sharing one must not overlap on the GPU. X is needed for the
+    weight gradients only and the weights for dX only; K comes from either."""
+    if dH.dim() != 2:
+        raise ValueError("dH must be 2-D")
+    if not dH.is_cuda:
+        raise ValueError("dH must be a CUDA tensor (no CPU path exists)")
+    if not (input_grad or weight_grad or bias_grad):
+        raise ValueError("no gradient is asked for")
+    M, N = dH.shape
+    dev = dH.device
+    src = X if X is not None else Wg
+    if src is None:
+        if input_grad or weight_grad:
+            raise ValueError("dX needs Wg and Wu, dWg and dWu need X")
+        K = 16  # the bias gradients alone do not depend on it
+    elif src.dim() != 2:
+        raise ValueError("X and the weights must be 2-D")
+    else:
+        K = src.shape[1]
+    f16 = torch.float16
+    if input_grad and (Wg is None or Wu is None):
+        raise ValueError("dX needs Wg and Wu")
+    if weight_grad and X is None:
+        raise ValueError("dWg and dWu need X")
+    pin = (_arg(dH, "dH", (M, N), f16, dev), _arg(G, "G", (M, N), f16, dev), _arg(U, "U", (M, N), f16, dev),
+           _arg(X, "X", (M, K), f16, dev), _arg(Wg, "Wg", (N, K), f16, dev), _arg(Wu, "Wu", (N, K), f16, dev))
+    if pin[1] is None or pin[2] is None:
+        raise ValueError("G and U are needed (qgemm_gated's save=)")
+    a = _act(act)
+    shapes = ((M, K), (N, K), (N, K), (N,), (N,))
+    asked = (input_grad, weight_grad, weight_grad, bias_grad, bias_grad)
+    names = ("dX", "dWg", "dWu", "dbg", "dbu")
+    if out is not None:
+        if len(out) != 5:
+            raise ValueError("out is (dX, dWg, dWu, dbg, dbu)")
+        for t, on, n, sh in zip(out, asked, names, shapes):
+            if (t is not None) != on:
+                raise ValueError(f"out: {n} is {'needed' if on else 'not asked for'}")
+            _arg(t, n, sh, f16, dev)
+    need = gated_backward_workspace_size(M, N)
+    if workspace is not None:
+        _arg(workspace, "workspace", workspace.shape, torch.uint8, dev)
+        if workspace.numel() < need:
+            raise ValueError(f"workspace of {workspace.numel()} bytes, {need} needed")
+    lib = load_library()
+    with _running_on(dev, stream) as raw:
+        if out is None:
+            out = tuple(torch.empty(sh, dtype=f16, device=dev) if on else None for on, sh in zip(asked, shapes))
+        ws = workspace if workspace is not None else torch.empty(need, dtype=torch.uint8, device=dev)
+        _check(lib.aria_gated_bwd(a, M, N, K, *pin, *(None if t is None else t.data_ptr() for t in out),
+                                  ws.data_ptr(), ws.numel(), raw))
+    return tuple(out)
 
 
 def selftest_bounded_wait(Xq, sx, Wq, sw, out=None, wait_limit_us: int = 50000, stream=None):

@@ -14,10 +14,13 @@
 #include <mutex>
 
 #include "aria_q.h"
+#include "act.cuh"
+#include "gated_bwd.cuh"
 #include "ptx.cuh"
 #include "qgemm.cuh"
 #include "quant_kernels.cuh"
 #include "smallm.cuh"
+#include "tgemm.cuh"
 
 #define ARIA_API extern "C" __attribute__((visibility("default")))
 
@@ -113,7 +116,9 @@ struct Plan {
   size_t smem;
 };
 
-aria_status plan_gemm(int kind, int64_t M, int64_t N, int64_t K, Plan* out) {
+// `epi`: aria::EpiMode. A gated tile holds 64 channels of either projection,
+// so its plan is that of a GEMM with 2 N weight rows.
+aria_status plan_gemm(int kind, int epi, int64_t M, int64_t N, int64_t K, Plan* out) {
   using namespace aria;
   const DevInfo di = dev_info();
   GemmParams p{};
@@ -139,7 +144,8 @@ aria_status plan_gemm(int kind, int64_t M, int64_t N, int64_t K, Plan* out) {
   };
   int bn = 0;
   int mt = tile_for(static_cast<int>((M + max_bn - 1) / max_bn), &bn);
-  const int nt = static_cast<int>((N + kTileN - 1) / kTileN);
+  const int chans = epi == kEpiGated ? tile_chans<kEpiGated>() : tile_chans<kEpiPlain>();
+  const int nt = static_cast<int>((N + chans - 1) / chans);
   // q8/q4 with a few hundred tokens: the dequant work per K block is the
   // same for any token tile, and a split-K launch costs several us of
   // cluster reduction. Measured at M = 432 (d = 1536 linears): prefer the
@@ -234,7 +240,7 @@ aria_status plan_gemm(int kind, int64_t M, int64_t N, int64_t K, Plan* out) {
   const uint32_t a_tile = ta ? 0u : kATile;
   const uint32_t out_bytes = kind == kS32 ? 4 : 2;
   const uint32_t epi_warps = dq ? 4 : 8;
-  const uint32_t stage_bytes = epi_warps * 2 * kEpiRows * 32 * out_bytes;  // 2 store boxes per warp
+  const uint32_t stage_bytes = epi_warps * warp_stage(epi, out_bytes);
   const uint32_t sxd_bytes = 2 * aria::kTileBnMax * 4;  // W8A8 token scales, two m-tiles
   p.x_stage = static_cast<uint32_t>(bn) * 128u;
   p.raw_stage = kind == kQ8 ? kATile : (kind == kQ4 ? kATile + kQ4ScaleTile : 0);
@@ -275,7 +281,7 @@ aria_status plan_gemm(int kind, int64_t M, int64_t N, int64_t K, Plan* out) {
   if (static_cast<uint32_t>(bn) * 512u > p.off_stage) p.splits = splits = 1;
   // warps 0..3 help with the last tile's epilogue when their store boxes (and
   // W8A8 token scales) fit in the activation ring
-  const uint64_t helper_bytes = 8ull * kEpiRows * 32 * out_bytes + 4ull * kTileBnMax;
+  const uint64_t helper_bytes = 4ull * warp_stage(epi, out_bytes) + 4ull * kTileBnMax;
   p.helpers = static_cast<uint64_t>(nx) * p.x_stage >= helper_bytes ? 1 : 0;
   const uint32_t nbar = 2 * (nr + na) + 6;  // raw, stage, 2 acc_full, 2 acc_empty, mma_drain, acc_last
   const size_t smem = 1024 + p.off_bar + nbar * 8 + 16;
@@ -311,7 +317,7 @@ void set_pdl(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr) {
 // how many clusters of `size` CTAs of this kernel can be resident at once on
 // the current device (cached per device, size and shared-memory footprint;
 // queried outside any capture on first use)
-template <int KIND>
+template <int KIND, int EPI>
 int max_clusters(int size, int threads, size_t smem) {
   static std::mutex mu;
   static int cache_dev[64], cache_size[64], cache_n[64];
@@ -333,7 +339,7 @@ int max_clusters(int size, int threads, size_t smem) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, aria::qgemm_kernel<KIND>, &cfg) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(&n, aria::qgemm_kernel<KIND, EPI>, &cfg) != cudaSuccess) {
     cudaGetLastError();
     n = 0;
   }
@@ -362,10 +368,11 @@ aria_status opt_in_smem(F* kfn, bool (&done)[kMaxDevices], std::mutex& mu) {
   return ARIA_OK;
 }
 
-template <int KIND>
+template <int KIND, int EPI = aria::kEpiPlain>
 aria_status launch_gemm(const Plan& pl, const CUtensorMap& tw, const CUtensorMap& ts,
-                        const CUtensorMap& tx, cudaStream_t st) {
-  auto kfn = aria::qgemm_kernel<KIND>;
+                        const CUtensorMap& tx, cudaStream_t st,
+                        const aria::GatedMaps<EPI>& tu = aria::GatedMaps<EPI>{}) {
+  auto kfn = aria::qgemm_kernel<KIND, EPI>;
   static bool attr_done[kMaxDevices] = {};
   static std::mutex attr_mu;
   aria_status as = opt_in_smem(kfn, attr_done, attr_mu);
@@ -379,7 +386,7 @@ aria_status launch_gemm(const Plan& pl, const CUtensorMap& tw, const CUtensorMap
   cudaLaunchAttribute attr[2];
   cfg.numAttrs = 0;
   // largest split whose clusters are all co-resident (one wave)
-  while (prm.splits > 1 && max_clusters<KIND>(prm.splits, pl.threads, pl.smem) < prm.tiles) --prm.splits;
+  while (prm.splits > 1 && max_clusters<KIND, EPI>(prm.splits, pl.threads, pl.smem) < prm.tiles) --prm.splits;
   if (prm.splits > 1) {
     cfg.gridDim = dim3(prm.splits, prm.tiles, 1);
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -391,7 +398,7 @@ aria_status launch_gemm(const Plan& pl, const CUtensorMap& tw, const CUtensorMap
   }
   set_pdl(cfg, attr);
   prm.trace_launch = next_trace_launch();
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kfn, tw, ts, tx, prm);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kfn, tw, ts, tx, prm, tu);
   if (e != cudaSuccess) return cuda_fail(e, "qgemm launch");
   return ARIA_OK;
 }
@@ -411,7 +418,7 @@ struct SmallPlan {
 constexpr int64_t kSmallMaxTokens = 16;
 constexpr size_t kSmallSmemBudget = 110 * 1024;  // two CTAs per SM
 
-template <int KIND, int TB, int CH, int GP>
+template <int KIND, int TB, int CH, int GP, int EPI>
 int small_max_clusters(int size, size_t smem) {
   static std::mutex mu;
   static int cache_dev[64], cache_size[64], cache_n[64];
@@ -433,7 +440,7 @@ int small_max_clusters(int size, size_t smem) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, aria::smallm_kernel<KIND, TB, CH, GP>, &cfg) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(&n, aria::smallm_kernel<KIND, TB, CH, GP, EPI>, &cfg) != cudaSuccess) {
     cudaGetLastError();
     n = 0;
   }
@@ -448,7 +455,8 @@ int small_max_clusters(int size, size_t smem) {
 }
 
 // shared-memory layout of a plan with `clusters` clusters of S CTAs
-bool small_layout(int kind, int64_t M, int64_t N, int64_t K, int S, int clusters, int tb, int gp,
+// (`rpc` weight rows per output channel: 2 for the gated epilogue)
+bool small_layout(int kind, int64_t M, int64_t N, int64_t K, int S, int clusters, int tb, int gp, int rpc,
                   aria::SmallParams* p, size_t* smem) {
   using namespace aria;
   const int num = kind == kF16 ? 2 : 1, den = kind == kQ4 ? 2 : 1;
@@ -456,7 +464,7 @@ bool small_layout(int kind, int64_t M, int64_t N, int64_t K, int S, int clusters
   p->kslice = static_cast<int>(K / S);
   p->rows_base = static_cast<int>(N / clusters);
   p->rows_rem = static_cast<int>(N % clusters);
-  const int rmax = p->rows_base + (p->rows_rem ? 1 : 0);
+  const int rmax = (p->rows_base + (p->rows_rem ? 1 : 0)) * rpc;
   p->r_pad = (rmax + 15) / 16 * 16;
   const uint32_t slice = static_cast<uint32_t>(p->kslice) * num / den;
   p->wrow = slice + 16;
@@ -475,11 +483,12 @@ bool small_layout(int kind, int64_t M, int64_t N, int64_t K, int S, int clusters
   return *smem <= kSmallSmemBudget;
 }
 
-template <int KIND, int TB, int CH, int GP>
+template <int KIND, int TB, int CH, int GP, int EPI>
 bool plan_small_t(int64_t M, int64_t N, int64_t K, SmallPlan* out) {
   using namespace aria;
   const DevInfo di = dev_info();
   const int unit = KIND == kQ4 ? 256 : 64;
+  constexpr int rpc = EPI == kEpiGated ? 2 : 1;
   if (K % unit) return false;
   int best_s = 0;
   for (int S = 1; S <= 8; ++S) {
@@ -494,13 +503,13 @@ bool plan_small_t(int64_t M, int64_t N, int64_t K, SmallPlan* out) {
   int clusters = static_cast<int>(std::min<int64_t>(di.sms / S, N));
   SmallParams p{};
   size_t smem = 0;
-  if (!small_layout(KIND, M, N, K, S, clusters, TB, GP, &p, &smem)) return false;
+  if (!small_layout(KIND, M, N, K, S, clusters, TB, GP, rpc, &p, &smem)) return false;
   if (S > 1) {
-    const int fit = small_max_clusters<KIND, TB, CH, GP>(S, smem);
+    const int fit = small_max_clusters<KIND, TB, CH, GP, EPI>(S, smem);
     if (fit < 1) return false;
     if (fit < clusters) {
       clusters = fit;
-      if (!small_layout(KIND, M, N, K, S, clusters, TB, GP, &p, &smem)) return false;
+      if (!small_layout(KIND, M, N, K, S, clusters, TB, GP, rpc, &p, &smem)) return false;
     }
   }
   p.M = static_cast<int>(M);
@@ -514,21 +523,22 @@ bool plan_small_t(int64_t M, int64_t N, int64_t K, SmallPlan* out) {
   return true;
 }
 
+template <int EPI>
 bool plan_small(int kind, int64_t M, int64_t N, int64_t K, SmallPlan* out) {
   using namespace aria;
   if (M > kSmallMaxTokens) return false;
   const bool two = M > 8;
   switch (kind) {
-    case kQ8: return two ? plan_small_t<kQ8, 2, 4, 2>(M, N, K, out) : plan_small_t<kQ8, 1, 6, 4>(M, N, K, out);
-    case kQ4: return two ? plan_small_t<kQ4, 2, 4, 2>(M, N, K, out) : plan_small_t<kQ4, 1, 6, 4>(M, N, K, out);
-    case kF16: return two ? plan_small_t<kF16, 2, 4, 2>(M, N, K, out) : plan_small_t<kF16, 1, 6, 4>(M, N, K, out);
+    case kQ8: return two ? plan_small_t<kQ8, 2, 4, 2, EPI>(M, N, K, out) : plan_small_t<kQ8, 1, 6, 4, EPI>(M, N, K, out);
+    case kQ4: return two ? plan_small_t<kQ4, 2, 4, 2, EPI>(M, N, K, out) : plan_small_t<kQ4, 1, 6, 4, EPI>(M, N, K, out);
+    case kF16: return two ? plan_small_t<kF16, 2, 4, 2, EPI>(M, N, K, out) : plan_small_t<kF16, 1, 6, 4, EPI>(M, N, K, out);
   }
   return false;
 }
 
-template <int KIND, int TB, int CH, int GP>
+template <int KIND, int TB, int CH, int GP, int EPI>
 aria_status launch_small_t(const SmallPlan& pl, cudaStream_t st) {
-  auto kfn = aria::smallm_kernel<KIND, TB, CH, GP>;
+  auto kfn = aria::smallm_kernel<KIND, TB, CH, GP, EPI>;
   static bool attr_done[kMaxDevices] = {};
   static std::mutex attr_mu;
   aria_status as = opt_in_smem(kfn, attr_done, attr_mu);
@@ -556,13 +566,14 @@ aria_status launch_small_t(const SmallPlan& pl, cudaStream_t st) {
   return ARIA_OK;
 }
 
+template <int EPI>
 aria_status launch_small(int kind, const SmallPlan& pl, cudaStream_t st) {
   using namespace aria;
   const bool two = pl.tb == 2;
   switch (kind) {
-    case kQ8: return two ? launch_small_t<kQ8, 2, 4, 2>(pl, st) : launch_small_t<kQ8, 1, 6, 4>(pl, st);
-    case kQ4: return two ? launch_small_t<kQ4, 2, 4, 2>(pl, st) : launch_small_t<kQ4, 1, 6, 4>(pl, st);
-    case kF16: return two ? launch_small_t<kF16, 2, 4, 2>(pl, st) : launch_small_t<kF16, 1, 6, 4>(pl, st);
+    case kQ8: return two ? launch_small_t<kQ8, 2, 4, 2, EPI>(pl, st) : launch_small_t<kQ8, 1, 6, 4, EPI>(pl, st);
+    case kQ4: return two ? launch_small_t<kQ4, 2, 4, 2, EPI>(pl, st) : launch_small_t<kQ4, 1, 6, 4, EPI>(pl, st);
+    case kF16: return two ? launch_small_t<kF16, 2, 4, 2, EPI>(pl, st) : launch_small_t<kF16, 1, 6, 4, EPI>(pl, st);
   }
   return fail(ARIA_ERR_INVALID_ARG, "unknown kind");
 }
@@ -699,12 +710,18 @@ struct SelfTest {
   int drop_first_stage = 0;
 };
 
-static aria_status qgemm_impl(int kind, int64_t M, int64_t N, int64_t K, const void* X,
-                              const float* sx, const void* Wq, const void* scales,
-                              const void* bias, const float* steer, float alpha,
-                              const float* alpha_dev, void* Y, cudaStream_t st,
-                              const void* xf16 = nullptr, const FusedWs* ws = nullptr,
-                              const SelfTest& selftest = SelfTest{}) {
+// what the kEpiAct and kEpiGated epilogues take besides a GEMM's arguments
+struct EpiArgs {
+  int act = ARIA_ACT_NONE;
+  const void* res = nullptr;     // kEpiAct
+  const void* Wu = nullptr;      // kEpiGated: the up projection
+  const void* scales_u = nullptr;
+  const void* bias_u = nullptr;
+  void* G = nullptr;             // kEpiGated: the pre-activations
+  void* U = nullptr;
+};
+
+static aria_status check_gemm_sizes(int kind, int64_t M, int64_t N, int64_t K) {
   using namespace aria;
   aria_status s = check_gemm_shape(M, N, K);
   if (s != ARIA_OK) return s;
@@ -713,9 +730,39 @@ static aria_status qgemm_impl(int kind, int64_t M, int64_t N, int64_t K, const v
   if ((kind == kW8A8 || kind == kS32) && K * 127 * 127 > INT32_MAX)
     return fail(ARIA_ERR_UNSUPPORTED, "int8 GEMM needs K * 127^2 < 2^31 (K <= %lld), got K=%lld",
                 (long long)(INT32_MAX / (127 * 127)), (long long)K);
+  return ARIA_OK;
+}
+
+// a weight's tensor maps: `rows` rows of 128 packed bytes (fp16: of 64
+// elements) per box, and for q4 the group scales
+static aria_status weight_maps(int kind, const void* W, const void* scales, int64_t N, int64_t K, int rows,
+                               CUtensorMap* tw, CUtensorMap* ts) {
+  using namespace aria;
+  aria_status s;
+  if (kind == kQ4) {
+    if ((s = make_map(tw, W, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, N, K / 2, 128, rows,
+                      CU_TENSOR_MAP_SWIZZLE_128B)) != ARIA_OK) return s;
+    return make_map(ts, scales, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, N, K / 32, 8, rows,
+                    CU_TENSOR_MAP_SWIZZLE_NONE);
+  }
+  if (kind == kF16)
+    return make_map(tw, W, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, N, K, 64, rows, CU_TENSOR_MAP_SWIZZLE_128B);
+  return make_map(tw, W, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, N, K, 128, rows, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <int EPI>
+static aria_status qgemm_impl(int kind, int64_t M, int64_t N, int64_t K, const void* X,
+                              const float* sx, const void* Wq, const void* scales,
+                              const void* bias, const float* steer, float alpha,
+                              const float* alpha_dev, void* Y, cudaStream_t st, const EpiArgs& ea,
+                              const void* xf16 = nullptr, const FusedWs* ws = nullptr,
+                              const SelfTest& selftest = SelfTest{}) {
+  using namespace aria;
+  aria_status s = check_gemm_sizes(kind, M, N, K);
+  if (s != ARIA_OK) return s;
   // a handful of tokens: the weight-streaming kernel, when its plan fits
   SmallPlan sp;
-  if (!xf16 && !selftest.drop_first_stage && plan_small(kind, M, N, K, &sp)) {
+  if (!xf16 && !selftest.drop_first_stage && plan_small<EPI>(kind, M, N, K, &sp)) {
     sp.p.W = static_cast<const uint8_t*>(Wq);
     sp.p.Wsc = kind == kQ4 ? static_cast<const __half*>(scales) : nullptr;
     sp.p.sw = kind == kQ8 ? static_cast<const float*>(scales) : nullptr;
@@ -725,24 +772,27 @@ static aria_status qgemm_impl(int kind, int64_t M, int64_t N, int64_t K, const v
     sp.p.alpha = sp.p.steer ? alpha : 0.0f;
     sp.p.alpha_dev = sp.p.steer ? alpha_dev : nullptr;
     sp.p.Y = static_cast<__half*>(Y);
-    return launch_small(kind, sp, st);
+    sp.p.act = ea.act;
+    sp.p.res = static_cast<const __half*>(ea.res);
+    sp.p.W_u = static_cast<const uint8_t*>(ea.Wu);
+    sp.p.Wsc_u = kind == kQ4 ? static_cast<const __half*>(ea.scales_u) : nullptr;
+    sp.p.sw_u = kind == kQ8 ? static_cast<const float*>(ea.scales_u) : nullptr;
+    sp.p.bias_u = static_cast<const __half*>(ea.bias_u);
+    sp.p.G = static_cast<__half*>(ea.G);
+    sp.p.U = static_cast<__half*>(ea.U);
+    return launch_small<EPI>(kind, sp, st);
   }
   Plan pl;
-  if ((s = plan_gemm(kind, M, N, K, &pl)) != ARIA_OK) return s;
+  if ((s = plan_gemm(kind, EPI, M, N, K, &pl)) != ARIA_OK) return s;
   CUtensorMap tw, ts, tx;
   std::memset(&ts, 0, sizeof(ts));
   const int bn = pl.p.BN;
-  if (kind == kQ4) {
-    if ((s = make_map(&tw, Wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, N, K / 2, 128, 128,
-                      CU_TENSOR_MAP_SWIZZLE_128B)) != ARIA_OK) return s;
-    if ((s = make_map(&ts, scales, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, N, K / 32, 8, 128,
-                      CU_TENSOR_MAP_SWIZZLE_NONE)) != ARIA_OK) return s;
-  } else if (kind == kF16) {
-    if ((s = make_map(&tw, Wq, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, N, K, 64, 128,
-                      CU_TENSOR_MAP_SWIZZLE_128B)) != ARIA_OK) return s;
-  } else {
-    if ((s = make_map(&tw, Wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, N, K, 128, 128,
-                      CU_TENSOR_MAP_SWIZZLE_128B)) != ARIA_OK) return s;
+  GatedMaps<EPI> tu;
+  const int wrows = tile_chans<EPI>();
+  if ((s = weight_maps(kind, Wq, scales, N, K, wrows, &tw, &ts)) != ARIA_OK) return s;
+  if constexpr (EPI == kEpiGated) {
+    std::memset(&tu, 0, sizeof(tu));
+    if ((s = weight_maps(kind, ea.Wu, ea.scales_u, N, K, wrows, &tu.W, &tu.S)) != ARIA_OK) return s;
   }
   if (kind == kQ8 || kind == kQ4 || kind == kF16) {
     if ((s = make_map(&tx, X, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, M, K, 64, bn,
@@ -769,12 +819,20 @@ static aria_status qgemm_impl(int kind, int64_t M, int64_t N, int64_t K, const v
     pl.p.gbar = ws->gbar;
     pl.p.sx = ws->sx;
   }
+  pl.p.act = ea.act;
+  pl.p.res = static_cast<const __half*>(ea.res);
+  pl.p.sw_u = static_cast<const float*>((kind == kQ4 || kind == kF16) ? nullptr : ea.scales_u);
+  pl.p.bias_u = static_cast<const __half*>(ea.bias_u);
+  pl.p.G = static_cast<__half*>(ea.G);
+  pl.p.U = static_cast<__half*>(ea.U);
   switch (kind) {
-    case kQ8: return launch_gemm<kQ8>(pl, tw, tw, tx, st);
-    case kQ4: return launch_gemm<kQ4>(pl, tw, ts, tx, st);
-    case kW8A8: return launch_gemm<kW8A8>(pl, tw, tw, tx, st);
-    case kS32: return launch_gemm<kS32>(pl, tw, tw, tx, st);
-    case kF16: return launch_gemm<kF16>(pl, tw, tw, tx, st);
+    case kQ8: return launch_gemm<kQ8, EPI>(pl, tw, tw, tx, st, tu);
+    case kQ4: return launch_gemm<kQ4, EPI>(pl, tw, ts, tx, st, tu);
+    case kW8A8: return launch_gemm<kW8A8, EPI>(pl, tw, tw, tx, st, tu);
+    case kF16: return launch_gemm<kF16, EPI>(pl, tw, tw, tx, st, tu);
+  }
+  if constexpr (EPI == kEpiPlain) {
+    if (kind == kS32) return launch_gemm<kS32>(pl, tw, tw, tx, st);
   }
   return fail(ARIA_ERR_INVALID_ARG, "unknown kind");
 }
@@ -816,8 +874,8 @@ ARIA_API aria_status aria_qgemm(aria_format fmt, int group, int64_t M, int64_t N
   int kind = 0;
   aria_status s = check_qgemm_args(fmt, group, X, sx, Wq, scales, bias, steer_vec, Y, &kind);
   if (s != ARIA_OK) return s;
-  return qgemm_impl(kind, M, N, K, X, sx, Wq, scales, bias, steer_vec, alpha, nullptr, Y,
-                    static_cast<cudaStream_t>(stream));
+  return qgemm_impl<aria::kEpiPlain>(kind, M, N, K, X, sx, Wq, scales, bias, steer_vec, alpha, nullptr, Y,
+                                     static_cast<cudaStream_t>(stream), EpiArgs{});
 }
 
 ARIA_API aria_status aria_qgemm_steer_dev(aria_format fmt, int group, int64_t M, int64_t N,
@@ -832,8 +890,8 @@ ARIA_API aria_status aria_qgemm_steer_dev(aria_format fmt, int group, int64_t M,
     return fail(ARIA_ERR_INVALID_ARG, "a steering vector needs a device alpha");
   if (alpha_dev && (reinterpret_cast<uintptr_t>(alpha_dev) & 3u))
     return fail(ARIA_ERR_MISALIGNED, "alpha_dev must be 4-byte aligned");
-  return qgemm_impl(kind, M, N, K, X, sx, Wq, scales, bias, steer_vec, 0.0f, alpha_dev, Y,
-                    static_cast<cudaStream_t>(stream));
+  return qgemm_impl<aria::kEpiPlain>(kind, M, N, K, X, sx, Wq, scales, bias, steer_vec, 0.0f, alpha_dev, Y,
+                                     static_cast<cudaStream_t>(stream), EpiArgs{});
 }
 
 ARIA_API aria_status aria_w8a8_workspace_size(int64_t M, int64_t K, size_t* bytes) {
@@ -863,8 +921,8 @@ ARIA_API aria_status aria_qgemm_w8a8_fused(int64_t M, int64_t N, int64_t K, cons
     return fail(ARIA_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes,
                 fused_ws_bytes(M, K));
   const FusedWs ws = fused_ws(workspace, M);
-  return qgemm_impl(aria::kW8A8, M, N, K, ws.xq, ws.sx, Wq, sw, bias, steer_vec, alpha, alpha_dev, Y,
-                    static_cast<cudaStream_t>(stream), X, &ws);
+  return qgemm_impl<aria::kEpiPlain>(aria::kW8A8, M, N, K, ws.xq, ws.sx, Wq, sw, bias, steer_vec, alpha, alpha_dev, Y,
+                                     static_cast<cudaStream_t>(stream), EpiArgs{}, X, &ws);
 }
 
 // ------------------------------------------------- no-allocation variant ---
@@ -917,8 +975,8 @@ ARIA_API aria_status aria_qgemm_w8a8_fused_noalloc(int64_t M, int64_t N, int64_t
   cudaError_t e = cudaMemsetAsync(scratch, 0, kWsHeader, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "clearing the static scratch's barrier");
   const FusedWs ws = fused_ws(scratch, M);
-  return qgemm_impl(aria::kW8A8, M, N, K, ws.xq, ws.sx, Wq, sw, bias, steer_vec, alpha, alpha_dev, Y,
-                    static_cast<cudaStream_t>(stream), X, &ws);
+  return qgemm_impl<aria::kEpiPlain>(aria::kW8A8, M, N, K, ws.xq, ws.sx, Wq, sw, bias, steer_vec, alpha, alpha_dev, Y,
+                                     static_cast<cudaStream_t>(stream), EpiArgs{}, X, &ws);
 }
 
 ARIA_API aria_status aria_qgemm_s32(int64_t M, int64_t N, int64_t K, const int8_t* Xq,
@@ -926,8 +984,8 @@ ARIA_API aria_status aria_qgemm_s32(int64_t M, int64_t N, int64_t K, const int8_
   if (!Xq || !Wq || !C) return fail(ARIA_ERR_INVALID_ARG, "NULL device pointer");
   if (!aligned16(Xq) || !aligned16(Wq) || !aligned16(C))
     return fail(ARIA_ERR_MISALIGNED, "device pointers must be 16-byte aligned");
-  return qgemm_impl(aria::kS32, M, N, K, Xq, nullptr, Wq, Wq, nullptr, nullptr, 0.0f, nullptr, C,
-                    static_cast<cudaStream_t>(stream));
+  return qgemm_impl<aria::kEpiPlain>(aria::kS32, M, N, K, Xq, nullptr, Wq, Wq, nullptr, nullptr, 0.0f, nullptr, C,
+                                     static_cast<cudaStream_t>(stream), EpiArgs{});
 }
 
 ARIA_API aria_status aria_selftest_bounded_wait(int64_t M, int64_t N, int64_t K, const int8_t* Xq,
@@ -943,8 +1001,304 @@ ARIA_API aria_status aria_selftest_bounded_wait(int64_t M, int64_t N, int64_t K,
   SelfTest t;
   t.wait_ns = static_cast<uint64_t>(wait_limit_us) * 1000u;
   t.drop_first_stage = 1;
-  return qgemm_impl(aria::kW8A8, M, N, K, Xq, sx, Wq, sw, nullptr, nullptr, 0.0f, nullptr, Y,
-                    static_cast<cudaStream_t>(stream), nullptr, nullptr, t);
+  return qgemm_impl<aria::kEpiPlain>(aria::kW8A8, M, N, K, Xq, sx, Wq, sw, nullptr, nullptr, 0.0f, nullptr, Y,
+                                     static_cast<cudaStream_t>(stream), EpiArgs{}, nullptr, nullptr, t);
+}
+
+// ------------------------------------------- feed-forward operators ---
+namespace {
+
+bool bad_act(int act) { return act < ARIA_ACT_NONE || act > ARIA_ACT_GELU_TANH; }
+
+// [a, a + na) and [b, b + nb) share a byte
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  if (!a || !b) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+// ---- the token-major kernel's plan and launch
+struct TgPlan {
+  aria::TgParams p;
+  aria::TgMaps m;
+  int cg = 1, grid = 0;
+  size_t smem = 0;
+};
+
+// Tiles, ring and shared-memory layout for R x C outputs of `nprob` problems,
+// `nkb` K blocks of `nsrc` sources. `bmn`: B is MN-major (boxes of 64).
+aria_status plan_tg(int mode, bool bmn, int cg, int bn, int splits, int64_t R, int64_t C, int64_t nkb, int nsrc,
+                    int nprob, TgPlan* out) {
+  using namespace aria;
+  const DevInfo di = dev_info();
+  TgParams p{};
+  p.R = static_cast<int>(R);
+  p.C = static_cast<int>(C);
+  p.nkb = static_cast<int>(nkb);
+  p.nsrc = nsrc;
+  p.BN = bn;
+  const int chans = mode == kTgGated ? bn / 2 : bn;
+  const int64_t tr = (R + kTgRows * cg - 1) / (kTgRows * cg), tc = (C + chans - 1) / chans;
+  const int64_t tiles = tr * tc * nprob;
+  if (tiles > (int64_t{1} << 30)) return fail(ARIA_ERR_UNSUPPORTED, "too many tiles");
+  p.tiles_r = static_cast<int>(tr);
+  p.tiles_c = static_cast<int>(tc);
+  p.tiles = static_cast<int>(tiles);
+  p.splits = splits;
+  const int bn_cta = bn / cg;
+  p.b_stage = static_cast<uint32_t>(bmn ? (bn_cta + 63) / 64 * 64 : bn_cta) * 128u;
+  const int64_t col_bytes = 2 * 3 * kTgAccCols * 4;
+  const int64_t budget = static_cast<int64_t>(di.smem_optin) - 1024 - 512 - col_bytes;
+  int ns = static_cast<int>(std::min<int64_t>(8, budget / (kTgATile + p.b_stage)));
+  if (ns < 2) return fail(ARIA_ERR_UNSUPPORTED, "tile does not fit in shared memory");
+  p.nstage = ns;
+  p.off_a = 0;
+  p.off_b = static_cast<uint32_t>(ns) * kTgATile;
+  p.off_col = p.off_b + static_cast<uint32_t>(ns) * p.b_stage;
+  // the split's partial tile (128 rows of bn + 4 words) overlays the rings
+  if (splits > 1) p.off_col = std::max(p.off_col, static_cast<uint32_t>(kTgRows * (bn + 4) * 4));
+  p.off_bar = p.off_col + static_cast<uint32_t>(col_bytes);
+  const size_t smem = 1024 + p.off_bar + (2 * ns + 5) * 8 + 16;
+  if (smem > static_cast<size_t>(di.smem_optin))
+    return fail(ARIA_ERR_UNSUPPORTED, "shared memory plan too large");
+  out->p = p;
+  out->cg = cg;
+  out->grid = splits > 1 ? static_cast<int>(tiles) * splits
+                         : cg * static_cast<int>(std::min<int64_t>(tiles, di.sms / cg));
+  out->smem = smem;
+  return ARIA_OK;
+}
+
+template <int MODE, bool I8, int CG, bool AMN, bool BMN>
+aria_status launch_tg_t(const TgPlan& pl, cudaStream_t st) {
+  auto kfn = aria::tgemm_kernel<MODE, I8, CG, AMN, BMN>;
+  static bool attr_done[kMaxDevices] = {};
+  static std::mutex attr_mu;
+  aria_status as = opt_in_smem(kfn, attr_done, attr_mu);
+  if (as != ARIA_OK) return as;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(pl.grid), 1, 1);
+  cfg.blockDim = dim3(aria::kTgThreads, 1, 1);
+  cfg.dynamicSmemBytes = pl.smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  const int cl = CG == 2 ? 2 : pl.p.splits;
+  if (cl > 1) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cl;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.numAttrs = 1;
+    cfg.attrs = attr;
+  }
+  set_pdl(cfg, attr);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kfn, pl.m, pl.p);
+  if (e != cudaSuccess) return cuda_fail(e, "token-major GEMM launch");
+  return ARIA_OK;
+}
+
+template <int MODE, bool I8, bool AMN, bool BMN>
+aria_status launch_tg(const TgPlan& pl, cudaStream_t st) {
+  return pl.cg == 2 ? launch_tg_t<MODE, I8, 2, AMN, BMN>(pl, st) : launch_tg_t<MODE, I8, 1, AMN, BMN>(pl, st);
+}
+
+aria_status half_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int box_rows) {
+  return make_map(m, base, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, rows, cols, 64, box_rows,
+                  CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// ---- the backward pass's workspace: dG, dU fp16 [M,N], then the column
+// partials fp32 [P][2N], each from a 256-byte boundary
+struct BwdLayout {
+  int rows = 16, P = 1;   // rows per block of the elementwise kernel, blocks along M
+  size_t off_du = 0, off_part = 0, bytes = 0;
+};
+
+BwdLayout bwd_layout(int64_t M, int64_t N) {
+  BwdLayout l;
+  // at most 64 partials per column (their sum is read once more), and at
+  // least 16 rows per block, one per row lane
+  l.rows = static_cast<int>(std::max<int64_t>(16, ((M + 63) / 64 + 15) / 16 * 16));
+  l.P = static_cast<int>((M + l.rows - 1) / l.rows);
+  auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+  l.off_du = up(static_cast<size_t>(M) * N * 2);
+  l.off_part = 2 * l.off_du;
+  l.bytes = l.off_part + up(static_cast<size_t>(l.P) * 2 * N * 4);
+  return l;
+}
+
+}  // namespace
+
+ARIA_API aria_status aria_qgemm_act(aria_format fmt, int group, int64_t M, int64_t N, int64_t K,
+                                    const void* X, const float* sx, const void* Wq, const void* scales,
+                                    const void* bias, aria_act act, const void* residual,
+                                    const float* steer_vec, float alpha, const float* alpha_dev, void* Y,
+                                    void* stream) {
+  int kind = 0;
+  aria_status s = check_qgemm_args(fmt, group, X, sx, Wq, scales, bias, steer_vec, Y, &kind);
+  if (s != ARIA_OK) return s;
+  if (bad_act(act)) return fail(ARIA_ERR_INVALID_ARG, "unknown activation %d", (int)act);
+  if (residual && !aligned16(residual))
+    return fail(ARIA_ERR_MISALIGNED, "device pointers must be 16-byte aligned");
+  if (alpha_dev && (reinterpret_cast<uintptr_t>(alpha_dev) & 3u))
+    return fail(ARIA_ERR_MISALIGNED, "alpha_dev must be 4-byte aligned");
+  if ((s = check_gemm_sizes(kind, M, N, K)) != ARIA_OK) return s;
+  const size_t yb = static_cast<size_t>(M) * N * 2;
+  if (residual != Y && overlap(residual, yb, Y, yb))
+    return fail(ARIA_ERR_INVALID_ARG, "the residual may be Y itself, but not overlap it otherwise");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (!steer_vec) alpha_dev = nullptr;
+  if (act == ARIA_ACT_NONE && !residual)  // the plain GEMM, byte for byte
+    return qgemm_impl<aria::kEpiPlain>(kind, M, N, K, X, sx, Wq, scales, bias, steer_vec, alpha, alpha_dev, Y,
+                                       st, EpiArgs{});
+  EpiArgs ea;
+  ea.act = act;
+  ea.res = residual;
+  return qgemm_impl<aria::kEpiAct>(kind, M, N, K, X, sx, Wq, scales, bias, steer_vec, alpha, alpha_dev, Y, st,
+                                   ea);
+}
+
+ARIA_API aria_status aria_qgemm_gated(aria_format fmt, int group, int64_t M, int64_t N, int64_t K,
+                                      const void* X, const float* sx, const void* Wg, const void* scales_g,
+                                      const void* Wu, const void* scales_u, const void* bias_g,
+                                      const void* bias_u, aria_act act, void* H, void* G, void* U,
+                                      void* stream) {
+  int kind = 0;
+  aria_status s = check_qgemm_args(fmt, group, X, sx, Wg, scales_g, bias_g, nullptr, H, &kind);
+  if (s != ARIA_OK) return s;
+  if ((s = check_qgemm_args(fmt, group, X, sx, Wu, scales_u, bias_u, nullptr, H, &kind)) != ARIA_OK) return s;
+  if (bad_act(act)) return fail(ARIA_ERR_INVALID_ARG, "unknown activation %d", (int)act);
+  if (!G != !U) return fail(ARIA_ERR_INVALID_ARG, "G and U are kept both or neither");
+  if ((G && !aligned16(G)) || (U && !aligned16(U)))
+    return fail(ARIA_ERR_MISALIGNED, "device pointers must be 16-byte aligned");
+  if ((s = check_gemm_sizes(kind, M, N, K)) != ARIA_OK) return s;
+  if (N > kMaxDim / 2) return fail(ARIA_ERR_UNSUPPORTED, "gated: N must be below 2^30");
+  const size_t yb = static_cast<size_t>(M) * N * 2;
+  if (overlap(G, yb, U, yb) || overlap(G, yb, H, yb) || overlap(U, yb, H, yb))
+    return fail(ARIA_ERR_INVALID_ARG, "H, G and U must not overlap");
+  EpiArgs ea;
+  ea.act = act;
+  ea.Wu = Wu;
+  ea.scales_u = scales_u;
+  ea.bias_u = bias_u;
+  ea.G = G;
+  ea.U = U;
+  return qgemm_impl<aria::kEpiGated>(kind, M, N, K, X, sx, Wg, scales_g, bias_g, nullptr, 0.0f, nullptr, H,
+                                     static_cast<cudaStream_t>(stream), ea);
+}
+
+ARIA_API aria_status aria_gated_bwd_workspace_size(int64_t M, int64_t N, size_t* bytes) {
+  if (!bytes) return fail(ARIA_ERR_INVALID_ARG, "NULL output pointer");
+  if (M < 1 || N < 1 || M > kMaxDim || N > kMaxDim)
+    return fail(ARIA_ERR_INVALID_ARG, "M and N must be in [1, 2^31)");
+  *bytes = bwd_layout(M, N).bytes;
+  return ARIA_OK;
+}
+
+ARIA_API aria_status aria_gated_bwd(aria_act act, int64_t M, int64_t N, int64_t K, const void* dH,
+                                    const void* G, const void* U, const void* X, const void* Wg,
+                                    const void* Wu, void* dX, void* dWg, void* dWu, void* dbg, void* dbu,
+                                    void* workspace, size_t workspace_bytes, void* stream) {
+  using namespace aria;
+  if (!dH || !G || !U || !workspace) return fail(ARIA_ERR_INVALID_ARG, "NULL device pointer");
+  if (!dWg != !dWu) return fail(ARIA_ERR_INVALID_ARG, "dWg and dWu are computed both or neither");
+  if (!dbg != !dbu) return fail(ARIA_ERR_INVALID_ARG, "dbg and dbu are computed both or neither");
+  if (!dX && !dWg && !dbg) return fail(ARIA_ERR_INVALID_ARG, "no output is asked for");
+  if (dX && (!Wg || !Wu)) return fail(ARIA_ERR_INVALID_ARG, "dX needs Wg and Wu");
+  if (dWg && !X) return fail(ARIA_ERR_INVALID_ARG, "dWg and dWu need X");
+  if (bad_act(act)) return fail(ARIA_ERR_INVALID_ARG, "unknown activation %d", (int)act);
+  for (const void* q : {dH, G, U, X, Wg, Wu, static_cast<const void*>(dX), static_cast<const void*>(dWg),
+                        static_cast<const void*>(dWu), static_cast<const void*>(dbg),
+                        static_cast<const void*>(dbu)})
+    if (q && !aligned16(q)) return fail(ARIA_ERR_MISALIGNED, "device pointers must be 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+    return fail(ARIA_ERR_MISALIGNED, "the workspace must be 256-byte aligned");
+  aria_status s = check_gemm_shape(M, N, K);
+  if (s != ARIA_OK) return s;
+  if (N > kMaxDim / 2) return fail(ARIA_ERR_UNSUPPORTED, "gated: N must be below 2^30");
+  const BwdLayout l = bwd_layout(M, N);
+  if (workspace_bytes < l.bytes)
+    return fail(ARIA_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes, l.bytes);
+  {
+    // outputs share no byte with an input, the workspace or one another
+    const size_t mn = static_cast<size_t>(M) * N * 2, mk = static_cast<size_t>(M) * K * 2,
+                 nk = static_cast<size_t>(N) * K * 2, nb = static_cast<size_t>(N) * 2;
+    const struct { const void* p; size_t n; } out[6] = {{dX, mk}, {dWg, nk}, {dWu, nk}, {dbg, nb}, {dbu, nb},
+                                                        {workspace, l.bytes}},
+        in[6] = {{dH, mn}, {G, mn}, {U, mn}, {X, mk}, {Wg, nk}, {Wu, nk}};
+    for (int i = 0; i < 6; ++i) {
+      for (int j = 0; j < 6; ++j)
+        if (overlap(out[i].p, out[i].n, in[j].p, in[j].n))
+          return fail(ARIA_ERR_INVALID_ARG, "an output or the workspace overlaps an input");
+      for (int j = i + 1; j < 6; ++j)
+        if (overlap(out[i].p, out[i].n, out[j].p, out[j].n))
+          return fail(ARIA_ERR_INVALID_ARG, "outputs and the workspace must not overlap");
+    }
+  }
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  __half* dG = (dX || dWg) ? reinterpret_cast<__half*>(ws) : nullptr;
+  __half* dU = (dX || dWg) ? reinterpret_cast<__half*>(ws + l.off_du) : nullptr;
+  float* part = dbg ? reinterpret_cast<float*>(ws + l.off_part) : nullptr;
+  {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    cfg.stream = st;
+    cfg.gridDim = dim3(static_cast<unsigned>((N + kGbCols - 1) / kGbCols), static_cast<unsigned>(l.P));
+    cfg.blockDim = dim3(kGbThreads);
+    set_pdl(cfg, attr);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, gated_bwd_kernel, static_cast<const __half*>(dH),
+                                       static_cast<const __half*>(G), static_cast<const __half*>(U), dG, dU, part,
+                                       static_cast<int>(M), static_cast<int>(N), l.rows, static_cast<int>(act));
+    if (e != cudaSuccess) return cuda_fail(e, "gated backward launch");
+  }
+  ColSum cs{part, static_cast<__half*>(dbg), static_cast<__half*>(dbu), l.P, static_cast<int>(N)};
+  const int sms = dev_info().sms;
+  if (dX) {
+    // k = 2 N: long, and the output tiles may be few
+    TgPlan pl;
+    const int64_t nkb = (N + 63) / 64;
+    const int64_t t = ((M + 127) / 128) * ((K + 127) / 128);
+    int splits = 1, bn = 256;
+    if (2 * t <= sms) {
+      bn = 128;
+      splits = static_cast<int>(std::min<int64_t>({kTgMaxSplits, sms / t, 2 * nkb}));
+    } else if (t <= 2 * sms) {
+      bn = 128;
+    }
+    if ((s = plan_tg(kTgStore, true, 1, bn, splits, M, K, nkb, 2, 1, &pl)) != ARIA_OK) return s;
+    pl.p.D[0] = static_cast<__half*>(dX);
+    if (!dWg) pl.p.colsum = cs;
+    if ((s = half_map(&pl.m.A[0], dG, M, N, kTgRows)) != ARIA_OK) return s;
+    if ((s = half_map(&pl.m.A[1], dU, M, N, kTgRows)) != ARIA_OK) return s;
+    if ((s = half_map(&pl.m.B[0], Wg, N, K, 64)) != ARIA_OK) return s;
+    if ((s = half_map(&pl.m.B[1], Wu, N, K, 64)) != ARIA_OK) return s;
+    if ((s = launch_tg<kTgStore, false, false, true>(pl, st)) != ARIA_OK) return s;
+  }
+  if (dWg) {
+    TgPlan pl;
+    if ((s = plan_tg(kTgStore, true, 1, 256, 1, N, K, (M + 63) / 64, 1, 2, &pl)) != ARIA_OK) return s;
+    pl.p.D[0] = static_cast<__half*>(dWg);
+    pl.p.D[1] = static_cast<__half*>(dWu);
+    pl.p.colsum = cs;
+    if ((s = half_map(&pl.m.A[0], dG, M, N, 64)) != ARIA_OK) return s;
+    if ((s = half_map(&pl.m.A[1], dU, M, N, 64)) != ARIA_OK) return s;
+    if ((s = half_map(&pl.m.B[0], X, M, K, 64)) != ARIA_OK) return s;
+    pl.m.B[1] = pl.m.B[0];
+    if ((s = launch_tg<kTgStore, false, true, true>(pl, st)) != ARIA_OK) return s;
+  }
+  if (dbg && !dX && !dWg) {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    cfg.stream = st;
+    cfg.gridDim = dim3(static_cast<unsigned>((2 * N + 255) / 256));
+    cfg.blockDim = dim3(256);
+    set_pdl(cfg, attr);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, colsum_kernel, static_cast<const float*>(part), cs.out0, cs.out1,
+                                       cs.P, cs.n);
+    if (e != cudaSuccess) return cuda_fail(e, "column sum launch");
+  }
+  return ARIA_OK;
 }
 
 ARIA_API aria_status aria_device_status(void* stream) {

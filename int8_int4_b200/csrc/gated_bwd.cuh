@@ -1,0 +1,121 @@
+// gated_bwd.cuh -- the elementwise part of the gated feed-forward's backward
+// pass:
+//
+//   dG = dH * U * act'(G),   dU = dH * act(G)
+//
+// from the kept pre-activations, and the column sums of both (the bias
+// gradients) from the unrounded fp32 values. dG and dU are rounded to fp16,
+// once: they are the operands of the two products that follow, and their
+// relative error of 2^-11 per element adds, independent from element to
+// element, about as much to those products as rounding their results does.
+//
+// Memory-bound: 6 bytes read and 4 written per element. A block covers 128
+// columns x `rows` rows, 16 threads along the columns (8 each, 16-byte
+// accesses) and 16 row lanes; a thread adds its columns over its rows, the
+// row lanes meet in shared memory, and each block leaves one row of
+// partials, which the last launch of the call adds in order (no atomics).
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cstdint>
+
+#include "act.cuh"
+#include "ptx.cuh"
+
+namespace aria {
+
+constexpr int kGbThreads = 256;
+constexpr int kGbCols = 128;
+
+__global__ void __launch_bounds__(kGbThreads)
+    gated_bwd_kernel(const __half* __restrict__ dH, const __half* __restrict__ G, const __half* __restrict__ U,
+                     __half* __restrict__ dG, __half* __restrict__ dU, float* __restrict__ part, int M, int N,
+                     int rows, int act) {
+  __shared__ float red[2][16][kGbCols];
+  pdl_wait();  // the inputs may come from the preceding kernel; the outputs may be in its hands
+  pdl_launch_dependents();
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int c = blockIdx.x * kGbCols + tx * 8;
+  const int rb = blockIdx.y * rows, re = rb + min(rows, M - rb);
+  float sg[8], su[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sg[i] = su[i] = 0.0f;
+  if (c < N) {  // N % 16 == 0: 8 columns are wholly in or out
+    with_act(act, [&](auto tag) {
+      constexpr int kUnroll = 2;
+      for (int r = rb + ty; r < re; r += 16 * kUnroll) {
+        uint4 vh[kUnroll], vg[kUnroll], vu[kUnroll];
+#pragma unroll
+        for (int q = 0; q < kUnroll; ++q) {
+          const int rq = r + 16 * q;
+          if (rq < re) {
+            const int64_t o = static_cast<int64_t>(rq) * N + c;
+            vh[q] = ld_dep_v4(dH + o);
+            vg[q] = ld_dep_v4(G + o);
+            vu[q] = ld_dep_v4(U + o);
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < kUnroll; ++q) {
+          const int rq = r + 16 * q;
+          if (rq >= re) break;
+          const __half2* h2 = reinterpret_cast<const __half2*>(&vh[q]);
+          const __half2* g2 = reinterpret_cast<const __half2*>(&vg[q]);
+          const __half2* u2 = reinterpret_cast<const __half2*>(&vu[q]);
+          uint4 og, ou;
+          __half2* og2 = reinterpret_cast<__half2*>(&og);
+          __half2* ou2 = reinterpret_cast<__half2*>(&ou);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 h = __half22float2(h2[i]), g = __half22float2(g2[i]), u = __half22float2(u2[i]);
+            float f0, d0, f1, d1;
+            act_fwd_bwd<decltype(tag)::value>(g.x, f0, d0);
+            act_fwd_bwd<decltype(tag)::value>(g.y, f1, d1);
+            const float a0 = h.x * u.x * d0, a1 = h.y * u.y * d1, b0 = h.x * f0, b1 = h.y * f1;
+            sg[2 * i] += a0;
+            sg[2 * i + 1] += a1;
+            su[2 * i] += b0;
+            su[2 * i + 1] += b1;
+            og2[i] = __floats2half2_rn(a0, a1);
+            ou2[i] = __floats2half2_rn(b0, b1);
+          }
+          const int64_t o = static_cast<int64_t>(rq) * N + c;
+          if (dG) {
+            *reinterpret_cast<uint4*>(dG + o) = og;
+            *reinterpret_cast<uint4*>(dU + o) = ou;
+          }
+        }
+      }
+    });
+  }
+  if (!part) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    red[0][ty][tx * 8 + i] = sg[i];
+    red[1][ty][tx * 8 + i] = su[i];
+  }
+  __syncthreads();
+  const int half = threadIdx.x >> 7, cc = threadIdx.x & 127;
+  const int col = blockIdx.x * kGbCols + cc;
+  if (col < N) {
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s += red[half][i][cc];
+    part[static_cast<int64_t>(blockIdx.y) * 2 * N + static_cast<int64_t>(half) * N + col] = s;
+  }
+}
+
+// The column sums alone, when no product follows that could add them.
+__global__ void __launch_bounds__(256) colsum_kernel(const float* __restrict__ part, __half* __restrict__ out0,
+                                                     __half* __restrict__ out1, int P, int n) {
+  pdl_wait();
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  if (c >= 2 * n) return;
+  float s = 0.0f;
+#pragma unroll 8
+  for (int i = 0; i < P; ++i) s += ld_dep_f32(part + static_cast<int64_t>(i) * 2 * n + c);
+  if (c < n) out0[c] = __float2half_rn(s);
+  else out1[c - n] = __float2half_rn(s);
+}
+
+}  // namespace aria

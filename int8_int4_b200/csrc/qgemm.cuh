@@ -46,12 +46,24 @@
 #include <cuda_fp16.h>
 #include <cstdint>
 
+#include "act.cuh"
 #include "ptx.cuh"
 #include "quant_kernels.cuh"
 
 namespace aria {
 
 enum GemmKind : int { kQ8 = 1, kQ4 = 2, kW8A8 = 3, kS32 = 4, kF16 = 5 };
+
+// What the epilogue computes (a template parameter: the plain GEMM's code is
+// not touched by the other two).
+//   kEpiPlain  y = main + bias + alpha v                    (aria_qgemm)
+//   kEpiAct    y = act(main + bias) + alpha v + R           (aria_qgemm_act)
+//   kEpiGated  h = act(main_g + bias_g) * (main_u + bias_u) (aria_qgemm_gated)
+// A gated tile holds 64 rows of the gate weight (TMEM lanes 0..63) and the 64
+// rows of the up weight for the same channels (lanes 64..127), so the
+// mainloop, the rings and the plans are those of a GEMM with 2 N rows; only
+// the epilogue brings the two halves of a channel together.
+enum EpiMode : int { kEpiPlain = 0, kEpiAct = 1, kEpiGated = 2 };
 
 constexpr int kTileN = 128;              // weight rows per tile (MMA M)
 constexpr uint32_t kATile = 16384;       // 128 rows x 128 bytes
@@ -98,6 +110,21 @@ struct GemmParams {
   int helpers;
   int trace_launch;       // trace builds: the launch's index since the trace was cleared
   void* Y;                // fp16 [M,N], or int32 [M,N] for kS32 (split-K path)
+  // kEpiAct, kEpiGated
+  int act;
+  const __half* res;      // kEpiAct: R [M,N] or null; may be Y itself
+  const float* sw_u;      // kEpiGated: the up projection's scales and bias
+  const __half* bias_u;   //            (sw and bias are the gate's)
+  __half* G;              // kEpiGated: the pre-activations [M,N], or null
+  __half* U;
+};
+
+// The up projection's tensor maps (kEpiGated); nothing otherwise.
+template <int EPI>
+struct GatedMaps {};
+template <>
+struct GatedMaps<kEpiGated> {
+  CUtensorMap W, S;
 };
 
 template <int KIND>
@@ -114,6 +141,18 @@ struct KindTraits {
   static constexpr uint32_t kOutBytes = KIND == kS32 ? 4 : 2;
   static constexpr uint32_t kStageBuf = kEpiRows * 32 * kOutBytes;  // one warp's store box
 };
+
+// output channels per tile
+template <int EPI>
+__host__ __device__ constexpr int tile_chans() { return EPI == kEpiGated ? kTileN / 2 : kTileN; }
+
+constexpr uint32_t kGatedExch = 8 * 32 * 4;  // one exchange box of a gated chunk: 8 tokens x 32 fp32
+
+// shared memory of one epilogue warp: two store boxes, or (gated) two
+// exchange boxes and one store box
+__host__ __device__ constexpr uint32_t warp_stage(int epi, uint32_t out_bytes) {
+  return epi == kEpiGated ? 2 * kGatedExch + kEpiRows * 32 * 2 : 2 * kEpiRows * 32 * out_bytes;
+}
 
 // ---------------------------------------------------------------- dequant ---
 __device__ __forceinline__ uint32_t h2_sub_mul(uint32_t v, uint32_t bias2, uint32_t s2) {
@@ -182,10 +221,16 @@ struct RowRaw {
   unsigned short bias = 0;  // fp16 bits
 };
 
-template <int KIND>
-__device__ __forceinline__ RowRaw row_raw(int n, const GemmParams& p) {
+template <int KIND, int EPI = kEpiPlain>
+__device__ __forceinline__ RowRaw row_raw(int n, const GemmParams& p, bool up = false) {
   RowRaw r;
   if (n >= p.N) return r;
+  if constexpr (EPI == kEpiGated) {
+    if constexpr (KIND == kW8A8 || KIND == kQ8) r.sw = __ldg((up ? p.sw_u : p.sw) + n);
+    const __half* b = up ? p.bias_u : p.bias;
+    if (b) r.bias = ld_dep_u16(b + n);
+    return r;
+  }
   if constexpr (KIND == kW8A8 || KIND == kQ8) r.sw = __ldg(p.sw + n);
   if (p.bias) r.bias = __half_as_ushort(p.bias[n]);
   if (p.steer) r.v = ld_dep_f32(p.steer + n);
@@ -225,6 +270,45 @@ __device__ __forceinline__ RowConst<KIND> row_const_from(const RowRaw& r, int n,
 template <int KIND>
 __device__ __forceinline__ RowConst<KIND> row_const(int n, const GemmParams& p) {
   return row_const_from<KIND>(row_raw<KIND>(n, p), n, p, p.steer ? steer_alpha(p) : 0.0f);
+}
+
+// The constants of the kEpiAct and kEpiGated epilogues, all in fp32: one
+// output channel's weight scale, bias and steering term.
+struct RowF {
+  float sw = 0.0f, bias = 0.0f, v = 0.0f, alpha = 0.0f;
+};
+
+__device__ __forceinline__ RowF row_f(const RowRaw& r, float alpha) {
+  RowF c;
+  c.sw = r.sw;
+  c.bias = __half2float(__ushort_as_half(r.bias));
+  c.v = r.v;
+  c.alpha = alpha;
+  return c;
+}
+
+// pre-activation of one element. W8A8: |acc| < 2^31 becomes fp32 with one
+// rounding (2^-24 relative), and the two scales and the bias add three more:
+// 2^-22 in all, a thousandth of the half step of the fp16 result. (The plain
+// W8A8 epilogue is rounded exactly; after an activation there is no exact
+// value to round to.)
+template <int KIND>
+__device__ __forceinline__ float pre_act(uint32_t acc, float sx, const RowF& c) {
+  float z;
+  if constexpr (KIND == kW8A8) {
+    z = __fmul_rn(__fmul_rn(__int2float_rn(static_cast<int32_t>(acc)), sx), c.sw);
+  } else {
+    z = __uint_as_float(acc);
+    if constexpr (KIND == kQ8) z = __fmul_rn(z, c.sw);
+  }
+  return __fadd_rn(z, c.bias);
+}
+
+// act(z) + alpha v; a zero strength leaves the value's bits alone
+template <int ACT>
+__device__ __forceinline__ float act_steer(float z, const RowF& c) {
+  const float y = act_fwd<ACT>(z);
+  return c.alpha != 0.0f ? __fmaf_rn(c.alpha, c.v, y) : y;
 }
 
 // W8A8 reference sequence: ((acc * s_x) * s_w) + bias + alpha*v in fp64, each
@@ -522,6 +606,252 @@ __device__ __forceinline__ int epilogue_chunks(int c_first, int cs, int nchunk, 
   return nst;
 }
 
+// -------------------------------------- epilogue with activation, residual ---
+// the residual's 16 x 32 box of chunk c, in the store's order: two 16-byte
+// pieces per lane
+__device__ __forceinline__ void residual_load(int c, int nb, int m0, int lane, const GemmParams& p,
+                                              uint4 (&rv)[2]) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int idx = j * 32 + lane;
+    const int m = m0 + c * 16 + (idx >> 2), n = nb + (idx & 3) * 8;
+    rv[j] = make_uint4(0u, 0u, 0u, 0u);
+    if (m < p.M && n < p.N) rv[j] = ld_dep_v4(p.res + static_cast<int64_t>(m) * p.N + n);
+  }
+}
+
+// kEpiAct: as epilogue_chunks. The residual of the next chunk is loaded while
+// this one is computed (a 16-byte load takes longer than a chunk), goes
+// through the store box to reach the lane that holds its channel, and is
+// replaced there by the result. Each element of R is read by the warp that
+// later writes the same element of Y, so Y may be R.
+template <int KIND, class Release>
+__device__ __forceinline__ void act_chunks(int c_first, int cs, int nchunk, uint32_t tacc, int lane,
+                                           uint8_t* sb0, const RowF& rc, const float* sxs, int nb,
+                                           int m0, const GemmParams& p, Release release) {
+  using T = KindTraits<KIND>;
+  if (c_first >= nchunk) {
+    release();
+    return;
+  }
+  uint4 rv[2];
+  if (p.res) residual_load(c_first, nb, m0, lane, p, rv);
+  int nst = 0;
+  for (int c = c_first; c < nchunk; c += cs, ++nst) {
+    uint8_t* sbuf = sb0 + (nst & 1) * T::kStageBuf;
+    __half* box = reinterpret_cast<__half*>(sbuf);
+    uint32_t r[16];
+    tmem_ld16(tacc + c * 16, r);
+    if (p.res) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) reinterpret_cast<uint4*>(sbuf)[j * 32 + lane] = rv[j];
+      if (c + cs < nchunk) residual_load(c + cs, nb, m0, lane, p, rv);
+      __syncwarp();
+    }
+    float sxv[16];
+    if constexpr (KIND == kW8A8) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float4 f = reinterpret_cast<const float4*>(sxs + c * 16)[q];
+        sxv[4 * q + 0] = f.x;
+        sxv[4 * q + 1] = f.y;
+        sxv[4 * q + 2] = f.z;
+        sxv[4 * q + 3] = f.w;
+      }
+    }
+    tmem_ld_wait();
+    if (c + cs >= nchunk) release();
+    with_act(p.act, [&](auto tag) {
+      if (p.res) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float y = act_steer<decltype(tag)::value>(pre_act<KIND>(r[i], KIND == kW8A8 ? sxv[i] : 0.0f, rc), rc);
+          box[i * 32 + lane] = __float2half_rn(__fadd_rn(y, __half2float(box[i * 32 + lane])));
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float y = act_steer<decltype(tag)::value>(pre_act<KIND>(r[i], KIND == kW8A8 ? sxv[i] : 0.0f, rc), rc);
+          box[i * 32 + lane] = __float2half_rn(y);
+        }
+      }
+    });
+    epilogue_chunk_store<KIND>(c, nb, m0, lane, sbuf, p);
+  }
+}
+
+// ------------------------------------------------------- gated epilogue ---
+// The warps of one epilogue group (4 warps, one per TMEM lane quarter) work
+// in pairs: warp q (0, 1) holds the gate's pre-activations of 32 channels,
+// warp q + 2 the up projection's of the same channels. They walk the same
+// chunks; for each, either warp hands over the half of the 16 tokens that
+// the other finishes (gate warp: tokens 0..7, up warp: 8..15).
+__device__ __forceinline__ uint32_t pair_bar_id(int warp) { return 3u + (warp >> 2) * 2u + (warp & 1); }
+
+// Both warps of the pair agree whether the accumulator is there: a warp that
+// gave up waiting must not leave its partner alone at the chunk barriers.
+__device__ __forceinline__ bool pair_all(int warp, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, %2, 64, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(ok)), "r"(pair_bar_id(warp))
+      : "memory");
+  return r != 0;
+}
+
+template <int ACT, int R>
+__device__ __forceinline__ void gated_out(const float (&own)[R], const float (&other)[R], bool up, __half (&h)[R]) {
+#pragma unroll
+  for (int j = 0; j < R; ++j) {
+    const float g = up ? other[j] : own[j], u = up ? own[j] : other[j];
+    h[j] = __float2half_rn(act_fwd<ACT>(g) * u);
+  }
+}
+
+template <int KIND, class Release>
+__device__ __forceinline__ void gated_chunks(int c_first, int cs, int nchunk, uint32_t tacc, int warp,
+                                             int lane, uint8_t* sb0, const RowF& rc, const float* sxs,
+                                             int nb, int m0, const GemmParams& p, Release release) {
+  constexpr uint32_t kWarpStage = warp_stage(kEpiGated, 2);
+  if (c_first >= nchunk) {
+    release();
+    return;
+  }
+  const bool up = (warp & 2) != 0;
+  const uint32_t bar = pair_bar_id(warp);
+  uint8_t* peer = up ? sb0 - 2 * kWarpStage : sb0 + 2 * kWarpStage;
+  __half* box = reinterpret_cast<__half*>(sb0 + 2 * kGatedExch);
+  int nst = 0;
+  for (int c = c_first; c < nchunk; c += cs, ++nst) {
+    uint32_t r[16];
+    tmem_ld16(tacc + c * 16, r);
+    float sxv[16];
+    if constexpr (KIND == kW8A8) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float4 f = reinterpret_cast<const float4*>(sxs + c * 16)[q];
+        sxv[4 * q + 0] = f.x;
+        sxv[4 * q + 1] = f.y;
+        sxv[4 * q + 2] = f.z;
+        sxv[4 * q + 3] = f.w;
+      }
+    }
+    tmem_ld_wait();
+    if (c + cs >= nchunk) release();
+    float z[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) z[i] = pre_act<KIND>(r[i], KIND == kW8A8 ? sxv[i] : 0.0f, rc);
+    // two exchange boxes: a warp writes one again only after the barrier of
+    // the chunk in between, which its partner reaches after reading it
+    const uint32_t eo = (nst & 1) * kGatedExch;
+    float* ex = reinterpret_cast<float*>(sb0 + eo);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ex[j * 32 + lane] = up ? z[j] : z[8 + j];
+    named_bar(bar, 64);
+    float own[8], other[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      own[j] = up ? z[8 + j] : z[j];
+      other[j] = reinterpret_cast<const float*>(peer + eo)[j * 32 + lane];
+    }
+    if (p.G) {  // a training step keeps the pre-activations
+#pragma unroll
+      for (int i = 0; i < 16; ++i) box[i * 32 + lane] = __float2half_rn(z[i]);
+      __syncwarp();
+      __half* Z = up ? p.U : p.G;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int idx = j * 32 + lane;
+        const int m = m0 + c * 16 + (idx >> 2), n = nb + (idx & 3) * 8;
+        const uint4 v = reinterpret_cast<const uint4*>(box)[idx];
+        if (m < p.M && n < p.N) *reinterpret_cast<uint4*>(Z + static_cast<int64_t>(m) * p.N + n) = v;
+      }
+      __syncwarp();
+    }
+    __half h[8];
+    with_act(p.act, [&](auto tag) { gated_out<decltype(tag)::value, 8>(own, other, up, h); });
+#pragma unroll
+    for (int j = 0; j < 8; ++j) box[j * 32 + lane] = h[j];
+    __syncwarp();
+    {
+      const int m = m0 + c * 16 + (up ? 8 : 0) + (lane >> 2), n = nb + (lane & 3) * 8;
+      const uint4 v = reinterpret_cast<const uint4*>(box)[lane];
+      if (m < p.M && n < p.N)
+        *reinterpret_cast<uint4*>(reinterpret_cast<__half*>(p.Y) + static_cast<int64_t>(m) * p.N + n) = v;
+    }
+    __syncwarp();  // the box has been read before the next chunk writes it
+  }
+}
+
+// Split-K: sum of the cluster's partials and the gated epilogue for token rows
+// [mb, me) of the tile. red[token][128] holds the gate's 64 channels, then
+// the up projection's. Lanes 0..15 of a warp take one token row, lanes
+// 16..31 the next, four channels each; partials are added in rank order.
+template <int KIND>
+__device__ __forceinline__ void split_gated(const uint8_t* red, int n0, int m0, int mb, int me, int warp,
+                                            int lane, const GemmParams& p) {
+  constexpr int kWarps = KindTraits<KIND>::kThreads / 32;
+  constexpr int kMaxSplits = 8;
+  const int nl = (lane & 15) * 4, n = n0 + nl;
+  RowF rg[4], ru[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    rg[j] = row_f(row_raw<KIND, kEpiGated>(n + j, p, false), 0.0f);
+    ru[j] = row_f(row_raw<KIND, kEpiGated>(n + j, p, true), 0.0f);
+  }
+  const uint32_t red_u32 = smem_u32(red);
+  for (int ml0 = mb + 2 * warp; ml0 < me; ml0 += 2 * kWarps) {
+    const int ml = ml0 + (lane >> 4);
+    const int m = m0 + ml;
+    if (ml >= me || m >= p.M || n >= p.N) continue;  // N % 16 == 0: 4 columns in range
+    const float sxm = KIND == kW8A8 ? ld_dep_f32(p.sx + m) : 0.0f;
+    uint4 vg[kMaxSplits], vu[kMaxSplits];
+#pragma unroll
+    for (int q = 0; q < kMaxSplits; ++q) {
+      if (q < p.splits) {
+        const uint32_t a = mapa_shared(red_u32 + static_cast<uint32_t>((ml * 128 + nl) * 4), q);
+        vg[q] = ld_dsmem_v4(a);
+        vu[q] = ld_dsmem_v4(a + 256u);
+      }
+    }
+    uint4 g = vg[0], u = vu[0];
+#pragma unroll
+    for (int q = 1; q < kMaxSplits; ++q) {
+      if (q < p.splits) {
+        g.x = reduce_add<KIND>(g.x, vg[q].x);
+        g.y = reduce_add<KIND>(g.y, vg[q].y);
+        g.z = reduce_add<KIND>(g.z, vg[q].z);
+        g.w = reduce_add<KIND>(g.w, vg[q].w);
+        u.x = reduce_add<KIND>(u.x, vu[q].x);
+        u.y = reduce_add<KIND>(u.y, vu[q].y);
+        u.z = reduce_add<KIND>(u.z, vu[q].z);
+        u.w = reduce_add<KIND>(u.w, vu[q].w);
+      }
+    }
+    const uint32_t g4[4] = {g.x, g.y, g.z, g.w}, u4[4] = {u.x, u.y, u.z, u.w};
+    float zg[4], zu[4];
+    __half h[4], hg[4], hu[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      zg[k] = pre_act<KIND>(g4[k], sxm, rg[k]);
+      zu[k] = pre_act<KIND>(u4[k], sxm, ru[k]);
+      hg[k] = __float2half_rn(zg[k]);
+      hu[k] = __float2half_rn(zu[k]);
+    }
+    with_act(p.act, [&](auto tag) { gated_out<decltype(tag)::value, 4>(zg, zu, false, h); });
+    const int64_t o = static_cast<int64_t>(m) * p.N + n;
+    *reinterpret_cast<uint2*>(reinterpret_cast<__half*>(p.Y) + o) = *reinterpret_cast<uint2*>(h);
+    if (p.G) {
+      *reinterpret_cast<uint2*>(p.G + o) = *reinterpret_cast<uint2*>(hg);
+      *reinterpret_cast<uint2*>(p.U + o) = *reinterpret_cast<uint2*>(hu);
+    }
+  }
+}
+
 // ----------------------------------------------- fused activation quant ---
 // "Results" (aria project page): W8A8 quantises the activations per token to
 // 8 bits. In the fused form every CTA of the GEMM quantises a share of the
@@ -624,11 +954,32 @@ __device__ __forceinline__ void fused_act_quant(const GemmParams& p, volatile in
 }
 
 // ------------------------------------------------------------------ kernel --
-template <int KIND>
+template <int KIND, int EPI = kEpiPlain>
 __global__ void __launch_bounds__(KindTraits<KIND>::kThreads, 1)
     qgemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmS,
-                 const __grid_constant__ CUtensorMap tmX, const GemmParams p) {
+                 const __grid_constant__ CUtensorMap tmX, const GemmParams p,
+                 const __grid_constant__ GatedMaps<EPI> tmU) {
   using T = KindTraits<KIND>;
+  constexpr int kChans = tile_chans<EPI>();  // output channels per tile
+  constexpr uint32_t kWarpStage = warp_stage(EPI, T::kOutBytes);
+  // one weight tile: 128 rows (gated: 64 rows of either projection) of the
+  // 128 packed bytes at x, and for q4 their group scales behind them
+  auto load_w = [&](uint64_t* bar, uint8_t* dst, int x, int n0, uint64_t pol) {
+    tma_load_2d(&tmW, bar, dst, x, n0, pol);
+    if constexpr (EPI == kEpiGated) tma_load_2d(&tmU.W, bar, dst + kATile / 2, x, n0, pol);
+  };
+  auto load_s = [&](uint64_t* bar, uint8_t* dst, int x, int n0, uint64_t pol) {
+    tma_load_2d(&tmS, bar, dst, x, n0, pol);
+    if constexpr (EPI == kEpiGated) tma_load_2d(&tmU.S, bar, dst + kQ4ScaleTile / 2, x, n0, pol);
+  };
+  auto prefetch_w = [&](int x, int n0) {
+    tma_prefetch_2d(&tmW, x, n0);
+    if constexpr (EPI == kEpiGated) tma_prefetch_2d(&tmU.W, x, n0);
+  };
+  auto prefetch_s = [&](int x, int n0) {
+    tma_prefetch_2d(&tmS, x, n0);
+    if constexpr (EPI == kEpiGated) tma_prefetch_2d(&tmU.S, x, n0);
+  };
   extern __shared__ uint8_t dyn_smem[];
   // 1024-byte alignment of the shared-window address (128-byte swizzle atoms)
   const uint32_t base_u32 = smem_u32(dyn_smem);
@@ -716,7 +1067,7 @@ __global__ void __launch_bounds__(KindTraits<KIND>::kThreads, 1)
       prefetch_tmap(&tmX);
       if constexpr (KIND == kQ4) prefetch_tmap(&tmS);
       if (pre > 0) {
-        const int n0 = (tile0 % p.tiles_n) * kTileN;
+        const int n0 = (tile0 % p.tiles_n) * kChans;
         const uint64_t pol = policy_evict_first();
         for (int i = 0; i < pre; ++i) {
           if constexpr (T::kDequant) {
@@ -724,21 +1075,21 @@ __global__ void __launch_bounds__(KindTraits<KIND>::kThreads, 1)
             uint8_t* dst = raw + i * p.raw_stage;
             if constexpr (KIND == kQ8) {
               mbar_arrive_expect_tx(raw_full + i, kATile);
-              tma_load_2d(&tmW, raw_full + i, dst, u * 128, n0, pol);
+              load_w(raw_full + i, dst, u * 128, n0, pol);
             } else {
               mbar_arrive_expect_tx(raw_full + i, kATile + kQ4ScaleTile);
-              tma_load_2d(&tmW, raw_full + i, dst, u * 128, n0, pol);
-              tma_load_2d(&tmS, raw_full + i, dst + kATile, u * 8, n0, pol);
+              load_w(raw_full + i, dst, u * 128, n0, pol);
+              load_s(raw_full + i, dst + kATile, u * 8, n0, pol);
             }
           } else {
             if (i == 0 && drop0) continue;  // self-test: this stage never fills
             mbar_arrive_expect_tx(st_full + i, kATile + p.x_stage);
-            tma_load_2d(&tmW, st_full + i, abuf + i * kATile, (u_begin + i) * T::kWUnitX, n0, pol);
+            load_w(st_full + i, abuf + i * kATile, (u_begin + i) * T::kWUnitX, n0, pol);
           }
         }
         for (int i = pre; i < nu && i < pre + kL2Ahead; ++i) {  // and the next units into L2
-          tma_prefetch_2d(&tmW, (u_begin + i) * T::kWUnitX, n0);
-          if constexpr (KIND == kQ4) tma_prefetch_2d(&tmS, (u_begin + i) * 8, n0);
+          prefetch_w((u_begin + i) * T::kWUnitX, n0);
+          if constexpr (KIND == kQ4) prefetch_s((u_begin + i) * 8, n0);
         }
       }
     }
@@ -888,6 +1239,30 @@ __global__ void __launch_bounds__(KindTraits<KIND>::kThreads, 1)
     return ok;
   };
 
+  // The CTA's last tile, for a warp that helps with it: the constants of the
+  // channel in its row t of the tile (loaded before the wait for the
+  // accumulator), and its chunks c0, c0 + cs, ...
+  auto tail_consts = [&](int t, int n0) {
+    if constexpr (EPI == kEpiPlain)
+      return row_const<KIND>(n0 + t, p);
+    else if constexpr (EPI == kEpiAct)
+      return row_f(row_raw<KIND>(n0 + t, p), p.steer ? steer_alpha(p) : 0.0f);
+    else
+      return row_f(row_raw<KIND, EPI>(n0 + (t & 63), p, t >= 64), 0.0f);
+  };
+  auto tail_chunks = [&](int c0, int cs, uint32_t tacc, uint8_t* sb0, const auto& rc, int n0, int m0,
+                         const float* sx_tile) {
+    // the last tile's buffer is not reused: nothing to release
+    if constexpr (EPI == kEpiPlain)
+      epilogue_chunks<KIND>(c0, cs, p.BN / 16, tacc, lane, sb0, 0, rc, sx_tile, n0 + (warp & 3) * 32, m0, p,
+                            [] {});
+    else if constexpr (EPI == kEpiAct)
+      act_chunks<KIND>(c0, cs, p.BN / 16, tacc, lane, sb0, rc, sx_tile, n0 + (warp & 3) * 32, m0, p, [] {});
+    else
+      gated_chunks<KIND>(c0, cs, p.BN / 16, tacc, warp, lane, sb0, rc, sx_tile, n0 + (warp & 1) * 32, m0, p,
+                         [] {});
+  };
+
   // The producer and MMA roles run as whole converged warps: every lane waits,
   // one lane issues (TMA by lane 0, MMA and commit by elect.sync), so the
   // issue loops stay warp-uniform. Ring slots and phases advance
@@ -900,7 +1275,7 @@ __global__ void __launch_bounds__(KindTraits<KIND>::kThreads, 1)
     int s = 0;
     uint32_t ph = 0;
     for (int tile = tile0; tile < p.tiles && ok; tile += tstep) {
-      const int n0 = (tile % p.tiles_n) * kTileN;
+      const int n0 = (tile % p.tiles_n) * kChans;
       if constexpr (T::kDequant) {
         for (int i = 0; i < nu; ++i) {
           if (tile == tile0 && i < pre) {  // issued before the dependency wait
@@ -912,16 +1287,16 @@ __global__ void __launch_bounds__(KindTraits<KIND>::kThreads, 1)
             uint8_t* dst = raw + s * p.raw_stage;
             const int u = u_begin + i;
             if (i + kL2Ahead < nu) {  // keep the weight stream kL2Ahead units ahead in L2
-              tma_prefetch_2d(&tmW, (u + kL2Ahead) * 128, n0);
-              if constexpr (KIND == kQ4) tma_prefetch_2d(&tmS, (u + kL2Ahead) * 8, n0);
+              prefetch_w((u + kL2Ahead) * 128, n0);
+              if constexpr (KIND == kQ4) prefetch_s((u + kL2Ahead) * 8, n0);
             }
             if constexpr (KIND == kQ8) {
               mbar_arrive_expect_tx(raw_full + s, kATile);
-              tma_load_2d(&tmW, raw_full + s, dst, u * 128, n0, pol);
+              load_w(raw_full + s, dst, u * 128, n0, pol);
             } else {
               mbar_arrive_expect_tx(raw_full + s, kATile + kQ4ScaleTile);
-              tma_load_2d(&tmW, raw_full + s, dst, u * 128, n0, pol);        // 256 k as bytes
-              tma_load_2d(&tmS, raw_full + s, dst + kATile, u * 8, n0, pol);  // 8 group scales
+              load_w(raw_full + s, dst, u * 128, n0, pol);          // 256 k as bytes
+              load_s(raw_full + s, dst + kATile, u * 8, n0, pol);  // 8 group scales
             }
           }
           ++issued_w;
@@ -945,9 +1320,9 @@ __global__ void __launch_bounds__(KindTraits<KIND>::kThreads, 1)
           wc_pe.stop();
           if (!ok) break;
           if (lane == 0) {
-            if (kb + kL2Ahead < nkb) tma_prefetch_2d(&tmW, (u_begin + kb + kL2Ahead) * T::kWUnitX, n0);
+            if (kb + kL2Ahead < nkb) prefetch_w((u_begin + kb + kL2Ahead) * T::kWUnitX, n0);
             mbar_arrive_expect_tx(st_full + s, kATile + p.x_stage);
-            tma_load_2d(&tmW, st_full + s, abuf + s * kATile, (u_begin + kb) * T::kWUnitX, n0, pol);
+            load_w(st_full + s, abuf + s * kATile, (u_begin + kb) * T::kWUnitX, n0, pol);
             tma_load_2d(&tmX, st_full + s, xbuf + s * p.x_stage, (u_begin + kb) * T::kXElemsPerKb, m0,
                         polx);
           }
@@ -1029,22 +1404,22 @@ __global__ void __launch_bounds__(KindTraits<KIND>::kThreads, 1)
       const bool ok = dequant_rows(t, 0, (KIND == kQ4 && p.tmem_a) ? 2 : 1);
       // The CTA's last tile: these warps take its odd epilogue chunks, with
       // store boxes staged in the now idle raw-weight ring.
-      if (ok && !split && tile0 < p.tiles) {
+      // (gated: its warps work in pairs, so one that gave up stays with its
+      // partner until they have agreed to skip the tile)
+      if ((ok || EPI == kEpiGated) && !split && tile0 < p.tiles) {
         const int ti = (p.tiles - tile0 + tstep - 1) / tstep - 1;
         const int tile = tile0 + ti * tstep;
         const int b = ti & 1;
-        const int n0 = (tile % p.tiles_n) * kTileN;
+        const int n0 = (tile % p.tiles_n) * kChans;
         const int m0 = (tile / p.tiles_n) * p.BN;
-        const RowConst<KIND> rc = row_const<KIND>(n0 + t, p);
-        bool ok2 = mbar_wait(acc_last, 0, abort_flag, 10, wlim);
+        const auto rc = tail_consts(t, n0);
+        bool ok2 = ok && mbar_wait(acc_last, 0, abort_flag, 10, wlim);
         ok2 = __all_sync(0xffffffffu, ok2);
+        if constexpr (EPI == kEpiGated) ok2 = pair_all(warp, ok2);
         if (ok2) {
           tc_fence_after();
           const uint32_t tacc = tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16) + b * kAccCols;
-          uint8_t* sb0 = raw + (warp - 8) * 2 * T::kStageBuf;
-          // the last tile's buffer is not reused: nothing to release
-          epilogue_chunks<KIND>(1, p.helpers ? 3 : 2, p.BN / 16, tacc, lane, sb0, 0, rc, sxs,
-                                n0 + (warp & 3) * 32, m0, p, [] {});
+          tail_chunks(1, p.helpers ? 3 : 2, tacc, raw + (warp - 8) * kWarpStage, rc, n0, m0, sxs);
         }
       }
     }
@@ -1066,14 +1441,16 @@ __global__ void __launch_bounds__(KindTraits<KIND>::kThreads, 1)
     const int cgrp = e >> 2, cstep = T::kEpiWarps >> 2;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     if (!split) {
-      uint8_t* sbuf0 = stage + e * 2 * T::kStageBuf;
+      uint8_t* sbuf0 = stage + e * kWarpStage;
+      const int tc = EPI == kEpiGated ? (t & 63) : t;  // channel within the tile
+      const bool up = EPI == kEpiGated && t >= 64;
       const float alpha = p.steer ? steer_alpha(p) : 0.0f;
       // The channel constants and (W8A8) token scales of a tile are loaded
       // one tile ahead, so their latency hides behind the previous tile's
       // epilogue; the token scales alternate between two shared buffers.
       RowRaw rr;
       if (tile0 < p.tiles) {
-        rr = row_raw<KIND>((tile0 % p.tiles_n) * kTileN + t, p);
+        rr = row_raw<KIND, EPI>((tile0 % p.tiles_n) * kChans + tc, p, up);
         if constexpr (KIND == kW8A8) {
           const int m0f = (tile0 / p.tiles_n) * p.BN;
           if (te < p.BN) sxs[te] = (m0f + te < p.M) ? ld_dep_f32(p.sx + m0f + te) : 0.0f;
@@ -1082,14 +1459,17 @@ __global__ void __launch_bounds__(KindTraits<KIND>::kThreads, 1)
       int ti = 0, nst = 0;
       for (int tile = tile0; tile < p.tiles; tile += tstep, ++ti) {
         const int b = ti & 1;
-        const int n0 = (tile % p.tiles_n) * kTileN;
+        const int n0 = (tile % p.tiles_n) * kChans;
         const int m0 = (tile / p.tiles_n) * p.BN;
-        const RowConst<KIND> rc = row_const_from<KIND>(rr, n0 + t, p, alpha);
+        RowConst<EPI == kEpiPlain ? KIND : kF16> rc;
+        RowF rf;
+        if constexpr (EPI == kEpiPlain) rc = row_const_from<KIND>(rr, n0 + t, p, alpha);
+        else rf = row_f(rr, alpha);
         const float* sxc = sxs + (ti & 1) * kTileBnMax;
         const int tnext = tile + tstep;
         float sx_next = 0.0f;
         if (tnext < p.tiles) {
-          rr = row_raw<KIND>((tnext % p.tiles_n) * kTileN + t, p);
+          rr = row_raw<KIND, EPI>((tnext % p.tiles_n) * kChans + tc, p, up);
           if constexpr (KIND == kW8A8) {
             const int m0n = (tnext / p.tiles_n) * p.BN;
             if (te < p.BN && m0n + te < p.M) sx_next = ld_dep_f32(p.sx + m0n + te);
@@ -1100,6 +1480,7 @@ __global__ void __launch_bounds__(KindTraits<KIND>::kThreads, 1)
         if constexpr (KIND == kW8A8) named_bar(1, nep);
         bool ok = mbar_wait(acc_full + b, (ti >> 1) & 1, abort_flag, 8, wlim);
         ok = __all_sync(0xffffffffu, ok);  // warp-uniform before .sync.aligned TMEM loads
+        if constexpr (EPI == kEpiGated) ok = pair_all(warp, ok);
         if (ok) {
           if (te == 0 && ti == 0) ARIA_STAMP(6);
           tc_fence_after();
@@ -1107,14 +1488,23 @@ __global__ void __launch_bounds__(KindTraits<KIND>::kThreads, 1)
           // take chunks too (see the end of the dequant role), and so do
           // warps 0..3 (see below)
           const int cs = tnext >= p.tiles ? (p.helpers ? 3 : (T::kDequant ? 2 : cstep)) : cstep;
-          nst = epilogue_chunks<KIND>(cgrp, cs, p.BN / 16, tmem_base + lane_off + b * kAccCols, lane, sbuf0,
-                                      nst, rc, sxc, n0 + (warp & 3) * 32, m0, p, [&] {
-                                        // this warp's last TMEM read of buffer b: the
-                                        // tile after next may reuse it
-                                        tc_fence_before();
-                                        __syncwarp();
-                                        if (lane == 0) mbar_arrive(acc_empty + b);
-                                      });
+          auto release = [&] {
+            // this warp's last TMEM read of buffer b: the tile after next may
+            // reuse it
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(acc_empty + b);
+          };
+          const uint32_t tacc = tmem_base + lane_off + b * kAccCols;
+          if constexpr (EPI == kEpiPlain)
+            nst = epilogue_chunks<KIND>(cgrp, cs, p.BN / 16, tacc, lane, sbuf0, nst, rc, sxc,
+                                        n0 + (warp & 3) * 32, m0, p, release);
+          else if constexpr (EPI == kEpiAct)
+            act_chunks<KIND>(cgrp, cs, p.BN / 16, tacc, lane, sbuf0, rf, sxc, n0 + (warp & 3) * 32, m0, p,
+                             release);
+          else
+            gated_chunks<KIND>(cgrp, cs, p.BN / 16, tacc, warp, lane, sbuf0, rf, sxc, n0 + (warp & 1) * 32, m0,
+                               p, release);
           if (te == 0) ARIA_STAMP(7);
         }
         // (on a failed wait, keep taking part in the named barriers of later tiles)
@@ -1133,11 +1523,11 @@ __global__ void __launch_bounds__(KindTraits<KIND>::kThreads, 1)
   if (warp < 4 && p.helpers && !split && tile0 < p.tiles) {
     const int ti = (p.tiles - tile0 + tstep - 1) / tstep - 1;
     const int tile = tile0 + ti * tstep;
-    const int n0 = (tile % p.tiles_n) * kTileN;
+    const int n0 = (tile % p.tiles_n) * kChans;
     const int m0 = (tile / p.tiles_n) * p.BN;
     const int t = warp * 32 + lane;  // weight row within the tile == TMEM lane
-    const RowConst<KIND> rc = row_const<KIND>(n0 + t, p);
-    float* hsx = reinterpret_cast<float*>(xbuf + 8 * T::kStageBuf);
+    const auto rc = tail_consts(t, n0);
+    float* hsx = reinterpret_cast<float*>(xbuf + 4 * kWarpStage);
     bool ok = mbar_wait(acc_last, 0, abort_flag, 10, wlim);
     ok = __all_sync(0xffffffffu, ok);
     if constexpr (KIND == kW8A8) {
@@ -1145,11 +1535,11 @@ __global__ void __launch_bounds__(KindTraits<KIND>::kThreads, 1)
         for (int j = threadIdx.x; j < p.BN; j += 128) hsx[j] = (m0 + j < p.M) ? ld_dep_f32(p.sx + m0 + j) : 0.0f;
       named_bar(2, 128);
     }
+    if constexpr (EPI == kEpiGated) ok = pair_all(warp, ok);
     if (ok) {
       tc_fence_after();
-      epilogue_chunks<KIND>(2, 3, p.BN / 16,
-                            tmem_base + (static_cast<uint32_t>(warp * 32) << 16) + (ti & 1) * kAccCols, lane,
-                            xbuf + warp * 2 * T::kStageBuf, 0, rc, hsx, n0 + warp * 32, m0, p, [] {});
+      tail_chunks(2, 3, tmem_base + (static_cast<uint32_t>(warp * 32) << 16) + (ti & 1) * kAccCols,
+                  xbuf + warp * kWarpStage, rc, n0, m0, hsx);
     }
   }
 
@@ -1185,16 +1575,34 @@ __global__ void __launch_bounds__(KindTraits<KIND>::kThreads, 1)
       constexpr int kWarps = KindTraits<KIND>::kThreads / 32;
       constexpr int kRows = 2;       // rows in flight per thread
       constexpr int kMaxSplits = 8;
-      const int n0 = (tile0 % p.tiles_n) * kTileN;
+      const int n0 = (tile0 % p.tiles_n) * kChans;
       const int m0 = (tile0 / p.tiles_n) * p.BN;
       const int mb = p.BN * rank / p.splits, me = p.BN * (rank + 1) / p.splits;
+      if constexpr (EPI == kEpiGated) {
+        split_gated<KIND>(smem, n0, m0, mb, me, warp, lane, p);
+      } else {
       const int nl = lane * 4;
       const int n = n0 + nl;
-      RowConst<KIND> rc[4];
+      RowConst<EPI == kEpiPlain ? KIND : kF16> rc[4];
+      RowF rf[4];
+      const float alpha = (EPI == kEpiAct && p.steer) ? steer_alpha(p) : 0.0f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) rc[j] = row_const<KIND>(n + j, p);
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (EPI == kEpiPlain) rc[j] = row_const<KIND>(n + j, p);
+        else rf[j] = row_f(row_raw<KIND>(n + j, p), alpha);
+      }
       const uint32_t red_u32 = smem_u32(smem);
       for (int ml0 = mb + warp; ml0 < me; ml0 += kRows * kWarps) {
+        uint2 rres[kRows];  // kEpiAct: the residual of this thread's channels
+        if constexpr (EPI == kEpiAct) {
+#pragma unroll
+          for (int u = 0; u < kRows; ++u) {
+            const int ml = ml0 + u * kWarps;
+            rres[u] = make_uint2(0u, 0u);
+            if (p.res && ml < me && m0 + ml < p.M && n < p.N)
+              rres[u] = ld_dep_v2(p.res + static_cast<int64_t>(m0 + ml) * p.N + n);
+          }
+        }
         uint4 v[kMaxSplits][kRows];
 #pragma unroll
         for (int q = 0; q < kMaxSplits; ++q) {
@@ -1233,7 +1641,17 @@ __global__ void __launch_bounds__(KindTraits<KIND>::kThreads, 1)
           } else {
             const uint32_t a4[4] = {acc[u].x, acc[u].y, acc[u].z, acc[u].w};
             __half h[4];
-            if constexpr (KIND == kW8A8) {
+            if constexpr (EPI == kEpiAct) {
+              const float sxm = KIND == kW8A8 ? ld_dep_f32(p.sx + m) : 0.0f;
+              const __half* hr = reinterpret_cast<const __half*>(&rres[u]);
+              with_act(p.act, [&](auto tag) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const float y = act_steer<decltype(tag)::value>(pre_act<KIND>(a4[k], sxm, rf[k]), rf[k]);
+                  h[k] = __float2half_rn(p.res ? __fadd_rn(y, __half2float(hr[k])) : y);
+                }
+              });
+            } else if constexpr (KIND == kW8A8) {
               const float sxm = ld_dep_f32(p.sx + m);
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
@@ -1256,7 +1674,7 @@ __global__ void __launch_bounds__(KindTraits<KIND>::kThreads, 1)
           }
         }
         if (threadIdx.x == 0 && ml0 == mb) ARIA_STAMP(21);  // their outputs stored
-        if constexpr (KIND == kW8A8) {
+        if constexpr (KIND == kW8A8 && EPI == kEpiPlain) {
           // rare elements: round exactly from the summed accumulator (picked
           // from registers by index: no second trip to the peers' shared
           // memory); these later stores of the same thread replace the
@@ -1283,6 +1701,7 @@ __global__ void __launch_bounds__(KindTraits<KIND>::kThreads, 1)
                 epi_w8a8(a, ld_dep_f32(p.sx + m), rk);
           }
         }
+      }
       }
     }
     ARIA_STAMP(9);

@@ -62,7 +62,60 @@ struct SmallParams {
   float alpha;
   const float* alpha_dev;
   __half* Y;              // [M,N]
+  // kEpiAct: activation and residual [M,N] (null: none; may be Y itself)
+  int act;
+  const __half* res;
+  // kEpiGated: the up projection (W, Wsc, sw and bias are the gate's), and
+  // the pre-activations [M,N] or null
+  const uint8_t* W_u;
+  const __half* Wsc_u;
+  const float* sw_u;
+  const __half* bias_u;
+  __half* G;
+  __half* U;
 };
+
+// The fused epilogue of one sum `s` of channel n and token t, q8 scale `sw`.
+template <int KIND, int EPI>
+__device__ __forceinline__ void small_epilogue(float s, float sw, int t, int n, float alpha,
+                                               const SmallParams& p) {
+  float y = s;
+  if constexpr (KIND == kQ8) y = __fmul_rn(y, sw);
+  const int64_t o = static_cast<int64_t>(t) * p.N + n;
+  if constexpr (EPI == kEpiPlain) {
+    if (p.bias) y = __fadd_rn(y, __half2float(p.bias[n]));
+    if (alpha != 0.0f) y = __fmaf_rn(alpha, ld_dep_f32(p.steer + n), y);
+    p.Y[o] = __float2half_rn(y);
+  } else {
+    const float r = p.res ? __half2float(__ushort_as_half(ld_dep_u16(p.res + o))) : 0.0f;
+    const float v = alpha != 0.0f ? ld_dep_f32(p.steer + n) : 0.0f;
+    if (p.bias) y = __fadd_rn(y, __half2float(__ushort_as_half(ld_dep_u16(p.bias + n))));
+    with_act(p.act, [&](auto tag) { y = act_fwd<decltype(tag)::value>(y); });
+    if (alpha != 0.0f) y = __fmaf_rn(alpha, v, y);
+    if (p.res) y = __fadd_rn(y, r);
+    p.Y[o] = __float2half_rn(y);
+  }
+}
+
+// gated: the sums of the gate's and the up projection's channel n
+template <int KIND>
+__device__ __forceinline__ void small_gated(float sg, float su, float swg, float swu, int t, int n,
+                                            const SmallParams& p) {
+  float g = sg, u = su;
+  if constexpr (KIND == kQ8) {
+    g = __fmul_rn(g, swg);
+    u = __fmul_rn(u, swu);
+  }
+  if (p.bias) g = __fadd_rn(g, __half2float(__ushort_as_half(ld_dep_u16(p.bias + n))));
+  if (p.bias_u) u = __fadd_rn(u, __half2float(__ushort_as_half(ld_dep_u16(p.bias_u + n))));
+  const int64_t o = static_cast<int64_t>(t) * p.N + n;
+  if (p.G) {
+    p.G[o] = __float2half_rn(g);
+    p.U[o] = __float2half_rn(u);
+  }
+  with_act(p.act, [&](auto tag) { g = act_fwd<decltype(tag)::value>(g); });
+  p.Y[o] = __float2half_rn(g * u);
+}
 
 template <int KIND>
 struct SmallTraits {
@@ -120,15 +173,21 @@ __device__ __forceinline__ void load_w16(const uint8_t* rowp, int kc, int q, uin
 // accumulated in registers per pass over the chunks.
 // At most 128 registers per thread (two CTAs per SM): a launch's CTAs can
 // then sit beside those of the preceding launch while both stream weights.
-template <int KIND, int TB, int CH, int GP>
+//
+// Gated (EPI): the cluster's R channels are 2 R weight rows, local row 2 j the
+// gate's and 2 j + 1 the up projection's row of channel j, so that a pass over
+// 16-row groups holds both sums of each of its channels.
+template <int KIND, int TB, int CH, int GP, int EPI = kEpiPlain>
 __global__ void __launch_bounds__(kSmThreads, 2) smallm_kernel(const SmallParams p) {
+  constexpr int RPC = EPI == kEpiGated ? 2 : 1;  // weight rows per channel
   using Tr = SmallTraits<KIND>;
   extern __shared__ __align__(128) uint8_t sm[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g4 = lane >> 2, q = lane & 3;
   const int rank = p.S > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int cl = blockIdx.x / p.S;
-  const int R = p.rows_base + (cl < p.rows_rem ? 1 : 0);
+  const int RC = p.rows_base + (cl < p.rows_rem ? 1 : 0);  // channels
+  const int R = RC * RPC;                                    // weight rows
   const int r0 = cl * p.rows_base + min(cl, p.rows_rem);
   const int k0 = rank * p.kslice;
   const uint32_t slice_bytes = static_cast<uint32_t>(p.kslice) * Tr::kNum / Tr::kDen;
@@ -151,18 +210,21 @@ __global__ void __launch_bounds__(kSmThreads, 2) smallm_kernel(const SmallParams
   {
     const uint64_t pol = policy_evict_first();  // streamed once
     for (int r = tid; r < R; r += kSmThreads) {
-      const int64_t n = r0 + r;
-      bulk_g2s(wsm + r * p.wrow, p.W + n * row_bytes + static_cast<int64_t>(k0) * Tr::kNum / Tr::kDen,
+      const int64_t n = r0 + r / RPC;
+      const uint8_t* W = (RPC == 2 && (r & 1)) ? p.W_u : p.W;
+      bulk_g2s(wsm + r * p.wrow, W + n * row_bytes + static_cast<int64_t>(k0) * Tr::kNum / Tr::kDen,
                slice_bytes, bar, pol);
       if constexpr (KIND == kQ4)
-        bulk_g2s(scs + r * (p.kslice / 32), p.Wsc + n * (p.K / 32) + k0 / 32, sc_bytes, bar, pol);
+        bulk_g2s(scs + r * (p.kslice / 32), ((RPC == 2 && (r & 1)) ? p.Wsc_u : p.Wsc) + n * (p.K / 32) + k0 / 32,
+                 sc_bytes, bar, pol);
     }
   }
   // q8: the channel scales of the CTA's rows (part of the pack, like the
   // weights) into shared memory, also before the wait
   float* s_sw = reinterpret_cast<float*>(sm + p.off_sw);
   if constexpr (KIND == kQ8)
-    for (int r = tid; r < R; r += kSmThreads) s_sw[r] = __ldg(p.sw + r0 + r);
+    for (int r = tid; r < R; r += kSmThreads)
+      s_sw[r] = __ldg(((RPC == 2 && (r & 1)) ? p.sw_u : p.sw) + r0 + r / RPC);
   if (tid == 0) ARIA_STAMP(1);
   pdl_launch_dependents();  // the next launch may start streaming its own weights
   pdl_wait();               // X, the epilogue operands and Y belong to the stream order
@@ -280,24 +342,35 @@ __global__ void __launch_bounds__(kSmThreads, 2) smallm_kernel(const SmallParams
     __syncthreads();
     // add the warps' partials in warp order: one output (token, row) per step
     const int prow = min(groups - gp, GP) * 16;
-    for (int idx = tid; idx < NT * prow; idx += kSmThreads) {
-      const int t = idx / prow, row = idx % prow;
-      const int rl = gp * 16 + row;  // row within the cluster's range
-      float s = 0.0f;
+    const float alpha = p.steer ? (p.alpha_dev ? *p.alpha_dev : p.alpha) : 0.0f;
+    if (EPI == kEpiGated && p.S == 1) {
+      // both sums of one channel per step
+      const int pch = prow / 2;
+      for (int idx = tid; idx < NT * pch; idx += kSmThreads) {
+        const int t = idx / pch, j = idx % pch;
+        const int rl = gp * 16 + 2 * j;
+        float sg = 0.0f, su = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kSmWarps; ++w) s += red[(w * NT + t) * rs + row];
-      if (p.S > 1) {
-        part[t * ps + rl] = s;
-      } else if (t < p.M && rl < R) {
-        const int n = r0 + rl;
-        float y = s;
-        if constexpr (KIND == kQ8) y = __fmul_rn(y, s_sw[rl]);
-        if (p.bias) y = __fadd_rn(y, __half2float(p.bias[n]));
-        if (p.steer) {
-          const float a = p.alpha_dev ? *p.alpha_dev : p.alpha;
-          if (a != 0.0f) y = __fmaf_rn(a, ld_dep_f32(p.steer + n), y);
+        for (int w = 0; w < kSmWarps; ++w) {
+          const float2 f = *reinterpret_cast<const float2*>(red + (w * NT + t) * rs + 2 * j);
+          sg += f.x;
+          su += f.y;
         }
-        p.Y[static_cast<int64_t>(t) * p.N + n] = __float2half_rn(y);
+        if (t < p.M && rl < R)
+          small_gated<KIND>(sg, su, KIND == kQ8 ? s_sw[rl] : 0.0f, KIND == kQ8 ? s_sw[rl + 1] : 0.0f, t,
+                            r0 + rl / 2, p);
+      }
+    } else {
+      for (int idx = tid; idx < NT * prow; idx += kSmThreads) {
+        const int t = idx / prow, row = idx % prow;
+        const int rl = gp * 16 + row;  // row within the cluster's range
+        float s = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kSmWarps; ++w) s += red[(w * NT + t) * rs + row];
+        if (p.S > 1)
+          part[t * ps + rl] = s;
+        else if (t < p.M && rl < R)
+          small_epilogue<KIND, EPI>(s, KIND == kQ8 ? s_sw[rl] : 0.0f, t, r0 + rl, alpha, p);
       }
     }
   }
@@ -307,22 +380,25 @@ __global__ void __launch_bounds__(kSmThreads, 2) smallm_kernel(const SmallParams
     // rank r finishes rows [R*r/S, R*(r+1)/S) of the cluster's range: the S
     // partials through distributed shared memory, added in rank order
     cluster_sync();
-    const int rb0 = R * rank / p.S, rb1 = R * (rank + 1) / p.S;
+    const int rb0 = RC * rank / p.S, rb1 = RC * (rank + 1) / p.S;  // channels
     const int nr = rb1 - rb0;
     if (tid == 0) ARIA_STAMP(5);
     const uint32_t part_u32 = smem_u32(sm + p.off_part);
     const float a = p.steer ? (p.alpha_dev ? *p.alpha_dev : p.alpha) : 0.0f;
     for (int idx = tid; idx < p.M * nr; idx += kSmThreads) {
-      const int t = idx / nr, rl = rb0 + idx % nr;
+      const int t = idx / nr, cc = rb0 + idx % nr;
+      const int rl = cc * RPC;
       const uint32_t off = static_cast<uint32_t>((t * ps + rl) * 4);
-      float s = 0.0f;
-      for (int r = 0; r < p.S; ++r) s += __uint_as_float(ld_dsmem_u32(mapa_shared(part_u32 + off, r)));
-      const int n = r0 + rl;
-      float y = s;
-      if constexpr (KIND == kQ8) y = __fmul_rn(y, s_sw[rl]);
-      if (p.bias) y = __fadd_rn(y, __half2float(p.bias[n]));
-      if (a != 0.0f) y = __fmaf_rn(a, ld_dep_f32(p.steer + n), y);
-      p.Y[static_cast<int64_t>(t) * p.N + n] = __float2half_rn(y);
+      float s = 0.0f, su = 0.0f;
+      for (int r = 0; r < p.S; ++r) {
+        const uint32_t pa = mapa_shared(part_u32 + off, r);
+        s += __uint_as_float(ld_dsmem_u32(pa));
+        if constexpr (RPC == 2) su += __uint_as_float(ld_dsmem_u32(pa + 4));
+      }
+      if constexpr (EPI == kEpiGated)
+        small_gated<KIND>(s, su, KIND == kQ8 ? s_sw[rl] : 0.0f, KIND == kQ8 ? s_sw[rl + 1] : 0.0f, t, r0 + cc, p);
+      else
+        small_epilogue<KIND, EPI>(s, KIND == kQ8 ? s_sw[rl] : 0.0f, t, r0 + cc, a, p);
     }
     cluster_sync();  // no CTA leaves while a peer still reads its partials
   }
