@@ -32,15 +32,21 @@ __device__ __forceinline__ float sigmoid(float z) { return fast_rcp(1.0f + __exp
 // to 2.8e-7 relative on [0, 8] (a least-squares fit reweighted toward equal
 // error, made in 64 bits for this file; 5.6e-7 when evaluated in fp32) and
 // keeps its a -> infinity limit. `gauss` returns exp(-a^2 / 2).
+__host__ __device__ constexpr float tail_coeff(int i) {
+  return i == 0 ? 0.10341634601354599f
+       : i == 1 ? 0.10833492130041122f
+       : i == 2 ? 0.06802142411470413f
+       : i == 3 ? 0.17879557609558105f
+       : i == 4 ? -0.12206314504146576f
+       : i == 5 ? 0.23910772800445557f
+                : -0.07561299204826355f;
+}
+
 __device__ __forceinline__ float normal_tail(float a, float& gauss) {
   const float t = fast_rcp(fmaf(0.26f, a, 1.0f));
-  float r = -0.07561299204826355f;
-  r = fmaf(r, t, 0.23910772800445557f);
-  r = fmaf(r, t, -0.12206314504146576f);
-  r = fmaf(r, t, 0.17879557609558105f);
-  r = fmaf(r, t, 0.06802142411470413f);
-  r = fmaf(r, t, 0.10833492130041122f);
-  r = fmaf(r, t, 0.10341634601354599f);
+  float r = tail_coeff(6);
+#pragma unroll
+  for (int i = 5; i >= 0; --i) r = fmaf(r, t, tail_coeff(i));
   gauss = __expf(-0.5f * a * a);
   return r * t * gauss;
 }
@@ -48,24 +54,92 @@ __device__ __forceinline__ float normal_tail(float a, float& gauss) {
 constexpr float kTanhC0 = 0.7978845608028654f;  // sqrt(2 / pi)
 constexpr float kTanhC1 = 0.044715f;
 
+// Two fp32 values in one 64-bit register: one issue slot per pair for the
+// sums and products. The epilogues of the wide tiles have as many
+// instructions per output as the mainloop leaves room for, and the pairs
+// halve their larger part.
+struct F2 {
+  uint64_t r;
+};
+
+__device__ __forceinline__ F2 f2(float x, float y) {
+  F2 v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v.r) : "f"(x), "f"(y));
+  return v;
+}
+__device__ __forceinline__ F2 f2(float x) { return f2(x, x); }
+__device__ __forceinline__ float2 f2_get(F2 v) {
+  float2 o;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(v.r));
+  return o;
+}
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
+  F2 v;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v.r) : "l"(a.r), "l"(b.r), "l"(c.r));
+  return v;
+}
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
+  F2 v;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v.r) : "l"(a.r), "l"(b.r));
+  return v;
+}
+__device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
+  F2 v;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v.r) : "l"(a.r), "l"(b.r));
+  return v;
+}
+
+__device__ __forceinline__ float fast_ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ F2 f2_ex2(F2 x) {
+  const float2 v = f2_get(x);
+  return f2(fast_ex2(v.x), fast_ex2(v.y));
+}
+__device__ __forceinline__ F2 f2_rcp(F2 x) {
+  const float2 v = f2_get(x);
+  return f2(fast_rcp(v.x), fast_rcp(v.y));
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// 1 / (1 + exp(-z)), z scaled by -log2(e) already
+__device__ __forceinline__ F2 f2_sigmoid_of(F2 neg_z_log2e) {
+  return f2_rcp(f2_add(f2_ex2(neg_z_log2e), f2(1.0f)));
+}
+
 template <int ACT>
-__device__ __forceinline__ float act_fwd(float z) {
+__device__ __forceinline__ F2 act_fwd2(F2 z) {
   if constexpr (ACT == kActRelu) {
-    return fmaxf(z, 0.0f);
+    const float2 v = f2_get(z);
+    return f2(fmaxf(v.x, 0.0f), fmaxf(v.y, 0.0f));
   } else if constexpr (ACT == kActSilu) {
-    return z * sigmoid(z);
+    return f2_mul(z, f2_sigmoid_of(f2_mul(z, f2(-kLog2e))));
   } else if constexpr (ACT == kActGelu) {
     // z Phi(z) = max(z, 0) - |z| Q(|z|): no cancellation on either side
-    const float a = fabsf(z);
-    float g;
-    return fmaf(-a, normal_tail(a, g), fmaxf(z, 0.0f));
+    const float2 v = f2_get(z);
+    const F2 a = f2(fabsf(v.x), fabsf(v.y));
+    const F2 t = f2_rcp(f2_fma(a, f2(0.26f), f2(1.0f)));
+    F2 r = f2(tail_coeff(6));
+#pragma unroll
+    for (int i = 5; i >= 0; --i) r = f2_fma(r, t, f2(tail_coeff(i)));
+    const F2 g = f2_ex2(f2_mul(f2_mul(a, f2(-0.5f * kLog2e)), a));
+    return f2_fma(f2_mul(f2_mul(r, t), f2(-1.0f)), f2_mul(a, g), f2(fmaxf(v.x, 0.0f), fmaxf(v.y, 0.0f)));
   } else if constexpr (ACT == kActGeluTanh) {
-    // z (1 + tanh w) / 2 = z sigmoid(2 w)
-    const float w2 = 2.0f * kTanhC0 * z * fmaf(kTanhC1 * z, z, 1.0f);
-    return z * sigmoid(w2);
+    // z (1 + tanh w) / 2 = z sigmoid(2 w), w = sqrt(2/pi) (z + 0.044715 z^3)
+    constexpr float k = -2.0f * kTanhC0 * kLog2e;
+    const F2 p = f2_fma(f2_mul(z, z), f2(k * kTanhC1), f2(k));
+    return f2_mul(z, f2_sigmoid_of(f2_mul(z, p)));
   } else {
     return z;
   }
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_fwd(float z) {
+  return f2_get(act_fwd2<ACT>(f2(z, z))).x;
 }
 
 // act(z) and act'(z)

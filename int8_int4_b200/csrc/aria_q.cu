@@ -1048,15 +1048,16 @@ aria_status plan_tg(int mode, bool bmn, int cg, int bn, int splits, int64_t R, i
   const int bn_cta = bn / cg;
   p.b_stage = static_cast<uint32_t>(bmn ? (bn_cta + 63) / 64 * 64 : bn_cta) * 128u;
   const int64_t col_bytes = 2 * 3 * kTgAccCols * 4;
-  const int64_t budget = static_cast<int64_t>(di.smem_optin) - 1024 - 512 - col_bytes;
+  const int64_t budget = static_cast<int64_t>(di.smem_optin) - 1024 - 512 - col_bytes - kTgStageBytes;
   int ns = static_cast<int>(std::min<int64_t>(8, budget / (kTgATile + p.b_stage)));
   if (ns < 2) return fail(ARIA_ERR_UNSUPPORTED, "tile does not fit in shared memory");
   p.nstage = ns;
   p.off_a = 0;
   p.off_b = static_cast<uint32_t>(ns) * kTgATile;
-  p.off_col = p.off_b + static_cast<uint32_t>(ns) * p.b_stage;
+  p.off_out = p.off_b + static_cast<uint32_t>(ns) * p.b_stage;
   // the split's partial tile (128 rows of bn + 4 words) overlays the rings
-  if (splits > 1) p.off_col = std::max(p.off_col, static_cast<uint32_t>(kTgRows * (bn + 4) * 4));
+  if (splits > 1) p.off_out = (std::max(p.off_out, static_cast<uint32_t>(kTgRows * (bn + 4) * 4)) + 1023u) & ~1023u;
+  p.off_col = p.off_out + kTgStageBytes;
   p.off_bar = p.off_col + static_cast<uint32_t>(col_bytes);
   const size_t smem = 1024 + p.off_bar + (2 * ns + 5) * 8 + 16;
   if (smem > static_cast<size_t>(di.smem_optin))
@@ -1107,6 +1108,57 @@ aria_status half_map(CUtensorMap* m, const void* base, int64_t rows, int64_t col
                   CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// an fp16 output [rows, cols] of the token-major kernel: 32 x 32 boxes
+aria_status out_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols) {
+  return make_map(m, base, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, rows, cols, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
+// The forward operators over many tokens (fp16, W8A8) on the token-major kernel.
+// Measured at N = 6144, K = 1536, M = 4096 against the channel-major kernel:
+// gated fp16 with G and U kept 121 against 203 us, gated W8A8 62 against 97.
+bool use_tg(int kind, int64_t M) {
+  return (kind == aria::kF16 || kind == aria::kW8A8) && M > 512;
+}
+
+template <int MODE>
+aria_status forward_tg(int kind, int64_t M, int64_t N, int64_t K, const void* X, const float* sx, const void* W,
+                       const void* scales, const void* bias, const float* steer, float alpha,
+                       const float* alpha_dev, void* Y, const EpiArgs& ea, cudaStream_t st) {
+  using namespace aria;
+  const bool i8 = kind == kW8A8;
+  TgPlan pl;
+  const int kelems = i8 ? 128 : 64;
+  aria_status s = plan_tg(MODE, false, 2, 256, 1, M, N, (K + kelems - 1) / kelems, 1, 1, &pl);
+  if (s != ARIA_OK) return s;
+  TgParams& p = pl.p;
+  p.act = ea.act;
+  p.sx = sx;
+  p.sw[0] = i8 ? static_cast<const float*>(scales) : nullptr;
+  p.sw[1] = i8 ? static_cast<const float*>(ea.scales_u) : nullptr;
+  p.bias[0] = static_cast<const __half*>(bias);
+  p.bias[1] = static_cast<const __half*>(ea.bias_u);
+  p.steer = (steer && (alpha_dev || alpha != 0.0f)) ? steer : nullptr;
+  p.alpha = p.steer ? alpha : 0.0f;
+  p.alpha_dev = p.steer ? alpha_dev : nullptr;
+  p.res = static_cast<const __half*>(ea.res);
+  p.save = ea.G != nullptr;
+  if ((s = out_map(&pl.m.D[0], Y, M, N)) != ARIA_OK) return s;
+  pl.m.D[1] = pl.m.D[2] = pl.m.D[0];
+  if (ea.G && ((s = out_map(&pl.m.D[1], ea.G, M, N)) != ARIA_OK || (s = out_map(&pl.m.D[2], ea.U, M, N)) != ARIA_OK))
+    return s;
+  const auto dt = i8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const int es = i8 ? 1 : 2;
+  const int brows = MODE == kTgGated ? p.BN / 2 : p.BN / pl.cg;  // rows of one B box
+  if ((s = make_map(&pl.m.A[0], X, dt, es, M, K, kelems, kTgRows, CU_TENSOR_MAP_SWIZZLE_128B)) != ARIA_OK) return s;
+  if ((s = make_map(&pl.m.B[0], W, dt, es, N, K, kelems, brows, CU_TENSOR_MAP_SWIZZLE_128B)) != ARIA_OK) return s;
+  pl.m.A[1] = pl.m.A[0];
+  pl.m.B[1] = pl.m.B[0];
+  if (MODE == kTgGated &&
+      (s = make_map(&pl.m.B[1], ea.Wu, dt, es, N, K, kelems, brows, CU_TENSOR_MAP_SWIZZLE_128B)) != ARIA_OK)
+    return s;
+  return i8 ? launch_tg<MODE, true, false, false>(pl, st) : launch_tg<MODE, false, false, false>(pl, st);
+}
+
 // ---- the backward pass's workspace: dG, dU fp16 [M,N], then the column
 // partials fp32 [P][2N], each from a 256-byte boundary
 struct BwdLayout {
@@ -1154,6 +1206,8 @@ ARIA_API aria_status aria_qgemm_act(aria_format fmt, int group, int64_t M, int64
   EpiArgs ea;
   ea.act = act;
   ea.res = residual;
+  if (use_tg(kind, M))
+    return forward_tg<aria::kTgAct>(kind, M, N, K, X, sx, Wq, scales, bias, steer_vec, alpha, alpha_dev, Y, ea, st);
   return qgemm_impl<aria::kEpiAct>(kind, M, N, K, X, sx, Wq, scales, bias, steer_vec, alpha, alpha_dev, Y, st,
                                    ea);
 }
@@ -1183,6 +1237,9 @@ ARIA_API aria_status aria_qgemm_gated(aria_format fmt, int group, int64_t M, int
   ea.bias_u = bias_u;
   ea.G = G;
   ea.U = U;
+  if (use_tg(kind, M))
+    return forward_tg<aria::kTgGated>(kind, M, N, K, X, sx, Wg, scales_g, bias_g, nullptr, 0.0f, nullptr, H, ea,
+                                      static_cast<cudaStream_t>(stream));
   return qgemm_impl<aria::kEpiGated>(kind, M, N, K, X, sx, Wg, scales_g, bias_g, nullptr, 0.0f, nullptr, H,
                                      static_cast<cudaStream_t>(stream), ea);
 }
@@ -1259,15 +1316,19 @@ ARIA_API aria_status aria_gated_bwd(aria_act act, int64_t M, int64_t N, int64_t 
     TgPlan pl;
     const int64_t nkb = (N + 63) / 64;
     const int64_t t = ((M + 127) / 128) * ((K + 127) / 128);
-    int splits = 1, bn = 256;
+    int splits = 1, bn = 256, cg = 2;
     if (2 * t <= sms) {
       bn = 128;
+      cg = 1;
       splits = static_cast<int>(std::min<int64_t>({kTgMaxSplits, sms / t, 2 * nkb}));
     } else if (t <= 2 * sms) {
       bn = 128;
+      cg = 1;
     }
-    if ((s = plan_tg(kTgStore, true, 1, bn, splits, M, K, nkb, 2, 1, &pl)) != ARIA_OK) return s;
+    if ((s = plan_tg(kTgStore, true, cg, bn, splits, M, K, nkb, 2, 1, &pl)) != ARIA_OK) return s;
     pl.p.D[0] = static_cast<__half*>(dX);
+    if ((s = out_map(&pl.m.D[0], dX, M, K)) != ARIA_OK) return s;
+    pl.m.D[1] = pl.m.D[2] = pl.m.D[0];
     if (!dWg) pl.p.colsum = cs;
     if ((s = half_map(&pl.m.A[0], dG, M, N, kTgRows)) != ARIA_OK) return s;
     if ((s = half_map(&pl.m.A[1], dU, M, N, kTgRows)) != ARIA_OK) return s;
@@ -1277,9 +1338,10 @@ ARIA_API aria_status aria_gated_bwd(aria_act act, int64_t M, int64_t N, int64_t 
   }
   if (dWg) {
     TgPlan pl;
-    if ((s = plan_tg(kTgStore, true, 1, 256, 1, N, K, (M + 63) / 64, 1, 2, &pl)) != ARIA_OK) return s;
-    pl.p.D[0] = static_cast<__half*>(dWg);
-    pl.p.D[1] = static_cast<__half*>(dWu);
+    if ((s = plan_tg(kTgStore, true, 2, 256, 1, N, K, (M + 63) / 64, 1, 2, &pl)) != ARIA_OK) return s;
+    if ((s = out_map(&pl.m.D[0], dWg, N, K)) != ARIA_OK) return s;
+    if ((s = out_map(&pl.m.D[1], dWu, N, K)) != ARIA_OK) return s;
+    pl.m.D[2] = pl.m.D[1];
     pl.p.colsum = cs;
     if ((s = half_map(&pl.m.A[0], dG, M, N, 64)) != ARIA_OK) return s;
     if ((s = half_map(&pl.m.A[1], dU, M, N, 64)) != ARIA_OK) return s;

@@ -53,8 +53,13 @@ constexpr uint32_t kTgATile = 16384;      // 128 rows x 64 fp16 (or 128 int8) of
 constexpr uint32_t kTgAccCols = 256;
 constexpr int kTgMaxSplits = 8;
 
+constexpr uint32_t kTgBox = 32 * 64;      // output box of a warp: 32 rows x 32 fp16
+constexpr int kTgSlots = 2;               // store boxes per epilogue warp
+constexpr uint32_t kTgStageBytes = kTgEpiWarps * kTgSlots * kTgBox;
+
 struct TgMaps {
   CUtensorMap A[2], B[2];
+  CUtensorMap D[3];  // outputs: one per problem; gated: H, G, U
 };
 
 // Column sums left over from an earlier kernel of the call: P rows of fp32
@@ -74,7 +79,7 @@ struct TgParams {
   int tiles_r, tiles_c, tiles;  // tiles: over all problems (tiles_r per problem)
   int nstage, splits;
   uint32_t b_stage;        // bytes of this CTA's part of a B tile
-  uint32_t off_a, off_b, off_col, off_bar;
+  uint32_t off_a, off_b, off_out, off_col, off_bar;
   // epilogue
   int act;
   const float* sx;         // int8: token scales [R]
@@ -84,9 +89,8 @@ struct TgParams {
   float alpha;
   const float* alpha_dev;
   const __half* res;       // kTgAct: [R,C] or null; may be D itself
-  __half* D[2];            // outputs, one per problem; kTgGated: D[0] = H
-  __half* G;               // kTgGated: pre-activations or null
-  __half* U;
+  __half* D[2];            // split-K: outputs, one per problem
+  int save;                // kTgGated: keep the pre-activations
   ColSum colsum;
 };
 
@@ -167,14 +171,39 @@ __device__ __forceinline__ void st_dsmem_wait_visible() {
   asm volatile("fence.acq_rel.cluster;" ::: "memory");
 }
 
-// 16 results of one row -> 32 bytes
-__device__ __forceinline__ void tg_store16(__half* dst, const float (&y)[16]) {
-  uint4 v[2];
-  __half2* h = reinterpret_cast<__half2*>(v);
+// 32 results of this lane's row -> its 64 bytes of the warp's store box
+// (64-byte swizzle: 16-byte piece j of row r at j ^ (r / 2 % 4), which spreads
+// eight lanes' stores over all banks)
+__device__ __forceinline__ void tg_box_row(uint8_t* box, int lane, const F2 (&y)[16]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) h[i] = __floats2half2_rn(y[2 * i], y[2 * i + 1]);
-  reinterpret_cast<uint4*>(dst)[0] = v[0];
-  reinterpret_cast<uint4*>(dst)[1] = v[1];
+  for (int j = 0; j < 4; ++j) {
+    uint4 v;
+    __half2* h = reinterpret_cast<__half2*>(&v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __float22half2_rn(f2_get(y[4 * j + i]));
+    *reinterpret_cast<uint4*>(box + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = v;
+  }
+}
+
+// fp32 pre-activations of 32 columns: accumulators, scales, bias
+template <bool I8>
+__device__ __forceinline__ void tg_pre(const uint32_t (&v)[32], float sx, const float* sw, const float* bias,
+                                       F2 (&z)[16]) {
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const float4 b = reinterpret_cast<const float4*>(bias)[q];
+    if constexpr (I8) {
+      const float4 s = reinterpret_cast<const float4*>(sw)[q];
+      const F2 x2 = f2(sx);
+      const F2 a0 = f2(__int2float_rn(static_cast<int32_t>(v[4 * q])), __int2float_rn(static_cast<int32_t>(v[4 * q + 1])));
+      const F2 a1 = f2(__int2float_rn(static_cast<int32_t>(v[4 * q + 2])), __int2float_rn(static_cast<int32_t>(v[4 * q + 3])));
+      z[2 * q] = f2_fma(f2_mul(a0, x2), f2(s.x, s.y), f2(b.x, b.y));
+      z[2 * q + 1] = f2_fma(f2_mul(a1, x2), f2(s.z, s.w), f2(b.z, b.w));
+    } else {
+      z[2 * q] = f2_add(f2(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1])), f2(b.x, b.y));
+      z[2 * q + 1] = f2_add(f2(__uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3])), f2(b.z, b.w));
+    }
+  }
 }
 
 // CG: CTAs sharing a tile (1 or 2). AMN, BMN: operand MN-major.
@@ -377,7 +406,8 @@ __global__ void __launch_bounds__(kTgThreads, 1)
     };
     float cv[3];
     col_load(unit, cv);
-    int ti = 0;
+    uint8_t* boxes = smem + p.off_out + e * (kTgSlots * kTgBox);
+    int ti = 0, nst = 0;
     for (int t = unit; t < p.tiles; t += nunit, ++ti) {
       const int b = ti & 1;
       int prob, r0, tc;
@@ -389,7 +419,7 @@ __global__ void __launch_bounds__(kTgThreads, 1)
         named_bar(1, kTgEpiWarps * 32);  // and every reader of this buffer two tiles ago is done
         col_load(t + nunit, cv);
       }
-      const int r = r0 + (warp & 3) * 32 + lane;
+      const int rw = r0 + (warp & 3) * 32, r = rw + lane;  // this warp's first row, this lane's row
       const bool row_in = r < p.R;
       const int64_t ro = static_cast<int64_t>(r) * p.C;
       float sx = 1.0f;
@@ -399,74 +429,79 @@ __global__ void __launch_bounds__(kTgThreads, 1)
       if (!ok) continue;  // (stays with the named barriers of later tiles)
       tc_fence_after();
       const uint32_t tacc = tmem_base + lane_off + b * kTgAccCols;
-      const int nchunk = chans / 16;
-      for (int c = cg; c < nchunk; c += 2) {
-        const int c0 = tc * chans + c * 16;
-        const bool in = row_in && c0 < p.C;  // C % 16 == 0: a chunk is wholly in or out
-        uint32_t v[16];
-        tmem_ld16(tacc + c * 16, v);
+      // units of 32 columns; a result goes through a store box of the warp's
+      // own and leaves by TMA, which clips the box at the tensor's edges
+      auto box_store = [&](const CUtensorMap* m, const F2 (&y)[16], int c0) {
+        uint8_t* box = boxes + (nst & (kTgSlots - 1)) * kTgBox;
+        ++nst;
+        if (lane == 0) bulk_wait_read<kTgSlots - 1>();  // the box's last store has read it
+        __syncwarp();
+        tg_box_row(box, lane, y);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (rw < p.R) tma_store_2d(m, box, c0, rw);
+          bulk_commit();
+        }
+      };
+      const int nunit32 = (chans + 31) / 32;
+      for (int c = cg; c < nunit32; c += 2) {
+        const int c0 = tc * chans + c * 32;
+        if (c0 >= p.C) break;
+        uint32_t v[32];
+        tmem_ld32(tacc + c * 32, v);
+        F2 z[16];
         if constexpr (MODE == kTgStore) {
           tmem_ld_wait();
-          float y[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(v[i]);
-          if (in) tg_store16(p.D[prob] + ro + c0, y);
+          for (int i = 0; i < 16; ++i) z[i] = f2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+          box_store(&tm.D[prob], z, c0);
         } else if constexpr (MODE == kTgAct) {
-          uint4 rv[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-          if (in && p.res) {
-            rv[0] = ld_dep_v4(p.res + ro + c0);
-            rv[1] = ld_dep_v4(p.res + ro + c0 + 8);
+          uint4 rv[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            rv[j] = make_uint4(0u, 0u, 0u, 0u);
+            if (p.res && row_in && c0 + 8 * j < p.C) rv[j] = ld_dep_v4(p.res + ro + c0 + 8 * j);  // C % 16 == 0
           }
           tmem_ld_wait();
-          float y[16];
-          const __half2* hr = reinterpret_cast<const __half2*>(rv);
+          tg_pre<I8>(v, sx, cb + kTgAccCols + c * 32, cb + c * 32, z);
           with_act(p.act, [&](auto tag) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float z = I8 ? __int2float_rn(static_cast<int32_t>(v[i])) * sx * cb[kTgAccCols + c * 16 + i]
-                           : __uint_as_float(v[i]);
-              z += cb[c * 16 + i];
-              y[i] = act_fwd<decltype(tag)::value>(z);
-            }
+            for (int i = 0; i < 16; ++i) z[i] = act_fwd2<decltype(tag)::value>(z[i]);
           });
           if (alpha != 0.0f) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) y[i] += cb[2 * kTgAccCols + c * 16 + i];
+            for (int q = 0; q < 8; ++q) {
+              const float4 f = reinterpret_cast<const float4*>(cb + 2 * kTgAccCols + c * 32)[q];
+              z[2 * q] = f2_add(z[2 * q], f2(f.x, f.y));
+              z[2 * q + 1] = f2_add(z[2 * q + 1], f2(f.z, f.w));
+            }
           }
           if (p.res) {
+            const __half2* hr = reinterpret_cast<const __half2*>(rv);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < 16; ++i) {
               const float2 f = __half22float2(hr[i]);
-              y[2 * i] += f.x;
-              y[2 * i + 1] += f.y;
+              z[i] = f2_add(z[i], f2(f.x, f.y));
             }
           }
-          if (in) tg_store16(p.D[0] + ro + c0, y);
+          box_store(&tm.D[0], z, c0);
         } else {
-          uint32_t w[16];
-          tmem_ld16(tacc + chans + c * 16, w);
+          uint32_t w[32];
+          tmem_ld32(tacc + chans + c * 32, w);
           tmem_ld_wait();
-          float g[16], u[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int k = c * 16 + i;
-            if constexpr (I8) {
-              g[i] = __int2float_rn(static_cast<int32_t>(v[i])) * sx * cb[kTgAccCols + k] + cb[k];
-              u[i] = __int2float_rn(static_cast<int32_t>(w[i])) * sx * cb[kTgAccCols + chans + k] + cb[chans + k];
-            } else {
-              g[i] = __uint_as_float(v[i]) + cb[k];
-              u[i] = __uint_as_float(w[i]) + cb[chans + k];
-            }
-          }
-          if (p.G && in) {
-            tg_store16(p.G + ro + c0, g);
-            tg_store16(p.U + ro + c0, u);
+          F2 u[16];
+          tg_pre<I8>(v, sx, cb + kTgAccCols + c * 32, cb + c * 32, z);
+          tg_pre<I8>(w, sx, cb + kTgAccCols + chans + c * 32, cb + chans + c * 32, u);
+          if (p.save) {
+            box_store(&tm.D[1], z, c0);
+            box_store(&tm.D[2], u, c0);
           }
           with_act(p.act, [&](auto tag) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) g[i] = act_fwd<decltype(tag)::value>(g[i]) * u[i];
+            for (int i = 0; i < 16; ++i) z[i] = f2_mul(act_fwd2<decltype(tag)::value>(z[i]), u[i]);
           });
-          if (in) tg_store16(p.D[0] + ro + c0, g);
+          box_store(&tm.D[0], z, c0);
         }
       }
       tc_fence_before();
@@ -476,6 +511,7 @@ __global__ void __launch_bounds__(kTgThreads, 1)
         else mbar_arrive(acc_empty + b);
       }
     }
+    if (lane == 0) bulk_wait_all();
   }
 
   // -------------------------------------------- split-K: cluster reduction
