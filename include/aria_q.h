@@ -236,10 +236,13 @@ aria_status aria_qgemm_gated(aria_format fmt, int group, int64_t M, int64_t N, i
 
 /*
  * aria_gated_bwd_workspace_size -- bytes of the workspace aria_gated_bwd needs
- * for M tokens and N channels (two fp16 [M,N] and at most 64 fp32 [2N]).
- * Errors: INVALID_ARG (NULL output, M or N outside [1, 2^31)).
+ * for M tokens, N channels and K input features, on the current device,
+ * whichever gradients are asked for: two fp16 [M,N], at most 64 fp32 [2N],
+ * and where few tokens make it worth splitting dX's sum over the channels, up
+ * to 16 fp32 [M,K].
+ * Errors: INVALID_ARG (NULL output, a size outside [1, 2^31)).
  */
-aria_status aria_gated_bwd_workspace_size(int64_t M, int64_t N, size_t *bytes);
+aria_status aria_gated_bwd_workspace_size(int64_t M, int64_t N, int64_t K, size_t *bytes);
 
 /*
  * aria_gated_bwd -- gradients of aria_qgemm_gated on fp16 weights
@@ -255,7 +258,7 @@ aria_status aria_gated_bwd_workspace_size(int64_t M, int64_t N, size_t *bytes);
  *              At least one output is asked for (INVALID_ARG). Every output is
  *              overwritten, not added to.
  *   workspace  caller-owned device memory, 256-byte aligned, at least
- *              aria_gated_bwd_workspace_size(M, N) bytes (INVALID_ARG
+ *              aria_gated_bwd_workspace_size(M, N, K) bytes (INVALID_ARG
  *              otherwise); its contents need no preparation and are
  *              unspecified afterwards. Calls that share one must not overlap
  *              on the GPU (one stream, or ordered by events).

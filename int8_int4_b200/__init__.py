@@ -70,7 +70,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "aria_qgemm_s32": ([I64, I64, I64, P, P, P, P], I),
         "aria_qgemm_act": ([I, I, I64, I64, I64, P, P, P, P, P, I, P, P, ctypes.c_float, P, P, P], I),
         "aria_qgemm_gated": ([I, I, I64, I64, I64, P, P, P, P, P, P, P, P, I, P, P, P, P], I),
-        "aria_gated_bwd_workspace_size": ([I64, I64, P], I),
+        "aria_gated_bwd_workspace_size": ([I64, I64, I64, P], I),
         "aria_gated_bwd": ([I, I64, I64, I64, P, P, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P], I),
         "aria_selftest_bounded_wait": ([I64, I64, I64, P, P, P, P, P, ctypes.c_uint32, P], I),
         "aria_device_status": ([P], I),
@@ -511,9 +511,9 @@ def qgemm_gated(fmt: str, X: torch.Tensor, Wg: torch.Tensor, scales_g, Wu: torch
     return out
 
 
-def gated_backward_workspace_size(M: int, N: int) -> int:
+def gated_backward_workspace_size(M: int, N: int, K: int) -> int:
     n = ctypes.c_size_t()
-    _check(load_library().aria_gated_bwd_workspace_size(M, N, ctypes.byref(n)))
+    _check(load_library().aria_gated_bwd_workspace_size(M, N, K, ctypes.byref(n)))
     return n.value
 
 
@@ -525,7 +525,7 @@ def gated_backward(dH: torch.Tensor, X, Wg, Wu, G: torch.Tensor, U: torch.Tensor
     dbg [N], dbu [N]), fp16, None for those not asked for.
 
     ``out``: a tuple of five tensors to write (None where nothing is asked
-    for). ``workspace``: a uint8 tensor of gated_backward_workspace_size(M, N)
+    for). ``workspace``: a uint8 tensor of gated_backward_workspace_size(M, N, K)
     bytes; calls sharing one must not overlap on the GPU. X is needed for the
     weight gradients only and the weights for dX only; K comes from either."""
     if dH.dim() != 2:
@@ -565,7 +565,7 @@ def gated_backward(dH: torch.Tensor, X, Wg, Wu, G: torch.Tensor, U: torch.Tensor
             if (t is not None) != on:
                 raise ValueError(f"out: {n} is {'needed' if on else 'not asked for'}")
             _arg(t, n, sh, f16, dev)
-    need = gated_backward_workspace_size(M, N)
+    need = gated_backward_workspace_size(M, N, K)
     if workspace is not None:
         _arg(workspace, "workspace", workspace.shape, torch.uint8, dev)
         if workspace.numel() < need:

@@ -22,16 +22,12 @@ __device__ __forceinline__ float fast_rcp(float x) {
   return r;
 }
 
-// 1 / (1 + exp(-z)). exp overflows to infinity below z = -88.7: the
-// reciprocal is then 0, as it should be to fp16.
-__device__ __forceinline__ float sigmoid(float z) { return fast_rcp(1.0f + __expf(-z)); }
-
 // Upper tail of the normal distribution, Q(a) = erfc(a / sqrt(2)) / 2 for
 // a >= 0, as exp(-a^2 / 2) * R(a): R = erfcx(a / sqrt(2)) / 2 is smooth and
 // slowly decreasing, and t * polynomial(t) in t = 1 / (1 + 0.26 a) fits it
 // to 2.8e-7 relative on [0, 8] (a least-squares fit reweighted toward equal
 // error, made in 64 bits for this file; 5.6e-7 when evaluated in fp32) and
-// keeps its a -> infinity limit. `gauss` returns exp(-a^2 / 2).
+// keeps its a -> infinity limit.
 __host__ __device__ constexpr float tail_coeff(int i) {
   return i == 0 ? 0.10341634601354599f
        : i == 1 ? 0.10833492130041122f
@@ -40,15 +36,6 @@ __host__ __device__ constexpr float tail_coeff(int i) {
        : i == 4 ? -0.12206314504146576f
        : i == 5 ? 0.23910772800445557f
                 : -0.07561299204826355f;
-}
-
-__device__ __forceinline__ float normal_tail(float a, float& gauss) {
-  const float t = fast_rcp(fmaf(0.26f, a, 1.0f));
-  float r = tail_coeff(6);
-#pragma unroll
-  for (int i = 5; i >= 0; --i) r = fmaf(r, t, tail_coeff(i));
-  gauss = __expf(-0.5f * a * a);
-  return r * t * gauss;
 }
 
 constexpr float kTanhC0 = 0.7978845608028654f;  // sqrt(2 / pi)
@@ -105,7 +92,18 @@ __device__ __forceinline__ F2 f2_rcp(F2 x) {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// 1 / (1 + exp(-z)), z scaled by -log2(e) already
+// Q(a), and exp(-a^2 / 2) in `gauss`
+__device__ __forceinline__ F2 normal_tail2(F2 a, F2& gauss) {
+  const F2 t = f2_rcp(f2_fma(a, f2(0.26f), f2(1.0f)));
+  F2 r = f2(tail_coeff(6));
+#pragma unroll
+  for (int i = 5; i >= 0; --i) r = f2_fma(r, t, f2(tail_coeff(i)));
+  gauss = f2_ex2(f2_mul(f2_mul(a, f2(-0.5f * kLog2e)), a));
+  return f2_mul(f2_mul(r, t), gauss);
+}
+
+// 1 / (1 + exp(-z)), z scaled by -log2(e) already. exp overflows to infinity
+// below z = -88.7: the reciprocal is then 0, as it should be to fp16.
 __device__ __forceinline__ F2 f2_sigmoid_of(F2 neg_z_log2e) {
   return f2_rcp(f2_add(f2_ex2(neg_z_log2e), f2(1.0f)));
 }
@@ -121,12 +119,8 @@ __device__ __forceinline__ F2 act_fwd2(F2 z) {
     // z Phi(z) = max(z, 0) - |z| Q(|z|): no cancellation on either side
     const float2 v = f2_get(z);
     const F2 a = f2(fabsf(v.x), fabsf(v.y));
-    const F2 t = f2_rcp(f2_fma(a, f2(0.26f), f2(1.0f)));
-    F2 r = f2(tail_coeff(6));
-#pragma unroll
-    for (int i = 5; i >= 0; --i) r = f2_fma(r, t, f2(tail_coeff(i)));
-    const F2 g = f2_ex2(f2_mul(f2_mul(a, f2(-0.5f * kLog2e)), a));
-    return f2_fma(f2_mul(f2_mul(r, t), f2(-1.0f)), f2_mul(a, g), f2(fmaxf(v.x, 0.0f), fmaxf(v.y, 0.0f)));
+    F2 g;
+    return f2_fma(f2_mul(a, f2(-1.0f)), normal_tail2(a, g), f2(fmaxf(v.x, 0.0f), fmaxf(v.y, 0.0f)));
   } else if constexpr (ACT == kActGeluTanh) {
     // z (1 + tanh w) / 2 = z sigmoid(2 w), w = sqrt(2/pi) (z + 0.044715 z^3)
     constexpr float k = -2.0f * kTanhC0 * kLog2e;
@@ -144,31 +138,35 @@ __device__ __forceinline__ float act_fwd(float z) {
 
 // act(z) and act'(z)
 template <int ACT>
-__device__ __forceinline__ void act_fwd_bwd(float z, float& f, float& d) {
+__device__ __forceinline__ void act_fwd_bwd2(F2 z, F2& f, F2& d) {
+  const F2 one = f2(1.0f), minus = f2(-1.0f);
   if constexpr (ACT == kActRelu) {
-    f = fmaxf(z, 0.0f);
-    d = z > 0.0f ? 1.0f : 0.0f;
+    const float2 v = f2_get(z);
+    f = f2(fmaxf(v.x, 0.0f), fmaxf(v.y, 0.0f));
+    d = f2(v.x > 0.0f ? 1.0f : 0.0f, v.y > 0.0f ? 1.0f : 0.0f);
   } else if constexpr (ACT == kActSilu) {
-    const float s = sigmoid(z);
-    f = z * s;
-    // 1 - s would cancel for large z; it multiplies z there, so the term's
-    // absolute error stays below fp32's step of the sum
-    d = s * fmaf(z, 1.0f - s, 1.0f);
+    // s + z s (1 - s): 1 - s cancels for large z, where it is a small part of
+    // the sum
+    const F2 s = f2_sigmoid_of(f2_mul(z, f2(-kLog2e)));
+    f = f2_mul(z, s);
+    d = f2_fma(f, f2_fma(s, minus, one), s);
   } else if constexpr (ACT == kActGelu) {
-    const float a = fabsf(z);
-    float g;
-    const float q = normal_tail(a, g);
-    f = fmaf(-a, q, fmaxf(z, 0.0f));
-    // Phi(z) + z phi(z)
-    d = fmaf(z * 0.3989422804014327f, g, z > 0.0f ? 1.0f - q : q);
+    // Phi(z) + z phi(z), Phi from the upper tail Q(|z|)
+    const float2 v = f2_get(z);
+    const F2 a = f2(fabsf(v.x), fabsf(v.y));
+    F2 g;
+    const float2 q = f2_get(normal_tail2(a, g));
+    f = f2_fma(f2_mul(a, minus), f2(q.x, q.y), f2(fmaxf(v.x, 0.0f), fmaxf(v.y, 0.0f)));
+    d = f2_fma(f2_mul(z, f2(0.3989422804014327f)), g, f2(v.x > 0.0f ? 1.0f - q.x : q.x, v.y > 0.0f ? 1.0f - q.y : q.y));
   } else if constexpr (ACT == kActGeluTanh) {
-    const float z2 = z * z;
-    const float s = sigmoid(2.0f * kTanhC0 * z * fmaf(kTanhC1, z2, 1.0f));
-    f = z * s;
-    d = fmaf(f * (1.0f - s), 2.0f * kTanhC0 * fmaf(3.0f * kTanhC1, z2, 1.0f), s);
+    constexpr float c = 2.0f * kTanhC0;
+    const F2 z2 = f2_mul(z, z);
+    const F2 s = f2_sigmoid_of(f2_mul(z, f2_fma(z2, f2(-c * kLog2e * kTanhC1), f2(-c * kLog2e))));
+    f = f2_mul(z, s);
+    d = f2_fma(f2_mul(f, f2_fma(s, minus, one)), f2_fma(z2, f2(3.0f * c * kTanhC1), f2(c)), s);
   } else {
     f = z;
-    d = 1.0f;
+    d = one;
   }
 }
 

@@ -1021,91 +1021,78 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
 struct TgPlan {
   aria::TgParams p;
   aria::TgMaps m;
-  int cg = 1, grid = 0;
+  int grid = 0;
   size_t smem = 0;
 };
 
-// Tiles, ring and shared-memory layout for R x C outputs of `nprob` problems,
-// `nkb` K blocks of `nsrc` sources. `bmn`: B is MN-major (boxes of 64).
-aria_status plan_tg(int mode, bool bmn, int cg, int bn, int splits, int64_t R, int64_t C, int64_t nkb, int nsrc,
-                    int nprob, TgPlan* out) {
+// Ring and shared-memory layout for tiles of 256 rows x `bn` accumulator
+// columns. `bmn`: B is MN-major (boxes of 64 columns).
+aria_status plan_tg(bool bmn, int bn, TgPlan* out) {
   using namespace aria;
   const DevInfo di = dev_info();
-  TgParams p{};
-  p.R = static_cast<int>(R);
-  p.C = static_cast<int>(C);
-  p.nkb = static_cast<int>(nkb);
-  p.nsrc = nsrc;
+  std::memset(&out->p, 0, sizeof(out->p));
+  std::memset(&out->m, 0, sizeof(out->m));
+  TgParams& p = out->p;
   p.BN = bn;
-  const int chans = mode == kTgGated ? bn / 2 : bn;
-  const int64_t tr = (R + kTgRows * cg - 1) / (kTgRows * cg), tc = (C + chans - 1) / chans;
-  const int64_t tiles = tr * tc * nprob;
-  if (tiles > (int64_t{1} << 30)) return fail(ARIA_ERR_UNSUPPORTED, "too many tiles");
-  p.tiles_r = static_cast<int>(tr);
-  p.tiles_c = static_cast<int>(tc);
-  p.tiles = static_cast<int>(tiles);
-  p.splits = splits;
-  const int bn_cta = bn / cg;
-  p.b_stage = static_cast<uint32_t>(bmn ? (bn_cta + 63) / 64 * 64 : bn_cta) * 128u;
+  p.b_stage = static_cast<uint32_t>(bmn ? (bn / 2 + 63) / 64 * 64 : bn / 2) * 128u;
   const int64_t col_bytes = 2 * 3 * kTgAccCols * 4;
   const int64_t budget = static_cast<int64_t>(di.smem_optin) - 1024 - 512 - col_bytes - kTgStageBytes;
-  int ns = static_cast<int>(std::min<int64_t>(8, budget / (kTgATile + p.b_stage)));
+  const int ns = static_cast<int>(std::min<int64_t>(8, budget / (kTgATile + p.b_stage)));
   if (ns < 2) return fail(ARIA_ERR_UNSUPPORTED, "tile does not fit in shared memory");
   p.nstage = ns;
   p.off_a = 0;
   p.off_b = static_cast<uint32_t>(ns) * kTgATile;
   p.off_out = p.off_b + static_cast<uint32_t>(ns) * p.b_stage;
-  // the split's partial tile (128 rows of bn + 4 words) overlays the rings
-  if (splits > 1) p.off_out = (std::max(p.off_out, static_cast<uint32_t>(kTgRows * (bn + 4) * 4)) + 1023u) & ~1023u;
   p.off_col = p.off_out + kTgStageBytes;
   p.off_bar = p.off_col + static_cast<uint32_t>(col_bytes);
-  const size_t smem = 1024 + p.off_bar + (2 * ns + 5) * 8 + 16;
-  if (smem > static_cast<size_t>(di.smem_optin))
+  out->smem = 1024 + p.off_bar + (2 * ns + 5) * 8 + 16;
+  if (out->smem > static_cast<size_t>(di.smem_optin))
     return fail(ARIA_ERR_UNSUPPORTED, "shared memory plan too large");
-  out->p = p;
-  out->cg = cg;
-  out->grid = splits > 1 ? static_cast<int>(tiles) * splits
-                         : cg * static_cast<int>(std::min<int64_t>(tiles, di.sms / cg));
-  out->smem = smem;
   return ARIA_OK;
 }
 
-template <int MODE, bool I8, int CG, bool AMN, bool BMN>
-aria_status launch_tg_t(const TgPlan& pl, cudaStream_t st) {
-  auto kfn = aria::tgemm_kernel<MODE, I8, CG, AMN, BMN>;
+template <int MODE, bool I8>
+aria_status launch_tg(TgPlan& pl, cudaStream_t st) {
+  auto kfn = aria::tgemm_kernel<MODE, I8>;
   static bool attr_done[kMaxDevices] = {};
   static std::mutex attr_mu;
   aria_status as = opt_in_smem(kfn, attr_done, attr_mu);
   if (as != ARIA_OK) return as;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(pl.grid), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * pl.p.nunit), 1, 1);
   cfg.blockDim = dim3(aria::kTgThreads, 1, 1);
   cfg.dynamicSmemBytes = pl.smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
-  const int cl = CG == 2 ? 2 : pl.p.splits;
-  if (cl > 1) {
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = cl;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.numAttrs = 1;
-    cfg.attrs = attr;
-  }
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.numAttrs = 1;
+  cfg.attrs = attr;
   set_pdl(cfg, attr);
   cudaError_t e = cudaLaunchKernelEx(&cfg, kfn, pl.m, pl.p);
   if (e != cudaSuccess) return cuda_fail(e, "token-major GEMM launch");
   return ARIA_OK;
 }
 
-template <int MODE, bool I8, bool AMN, bool BMN>
-aria_status launch_tg(const TgPlan& pl, cudaStream_t st) {
-  return pl.cg == 2 ? launch_tg_t<MODE, I8, 2, AMN, BMN>(pl, st) : launch_tg_t<MODE, I8, 1, AMN, BMN>(pl, st);
-}
-
 aria_status half_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int box_rows) {
   return make_map(m, base, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, rows, cols, 64, box_rows,
                   CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// fp32 partials [parts][rows][cols]: 32 x 32 boxes of one part
+aria_status partial_map(CUtensorMap* m, const void* base, int parts, int64_t rows, int64_t cols) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return fail(ARIA_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(parts)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols) * 4, static_cast<cuuint64_t>(rows) * cols * 4};
+  cuuint32_t box[3] = {32, 32, 1}, estr[3] = {1, 1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(ARIA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return ARIA_OK;
 }
 
 // an fp16 output [rows, cols] of the token-major kernel: 32 x 32 boxes
@@ -1128,9 +1115,18 @@ aria_status forward_tg(int kind, int64_t M, int64_t N, int64_t K, const void* X,
   const bool i8 = kind == kW8A8;
   TgPlan pl;
   const int kelems = i8 ? 128 : 64;
-  aria_status s = plan_tg(MODE, false, 2, 256, 1, M, N, (K + kelems - 1) / kelems, 1, 1, &pl);
+  aria_status s = plan_tg(false, 256, &pl);
   if (s != ARIA_OK) return s;
   TgParams& p = pl.p;
+  const int chans = MODE == kTgGated ? p.BN / 2 : p.BN;
+  const int64_t tr = (M + 2 * kTgRows - 1) / (2 * kTgRows), tiles = tr * ((N + chans - 1) / chans);
+  if (tiles > (int64_t{1} << 30)) return fail(ARIA_ERR_UNSUPPORTED, "too many tiles");
+  p.R = static_cast<int>(M);
+  p.C = static_cast<int>(N);
+  p.nkb = static_cast<int>((K + kelems - 1) / kelems);
+  p.tiles_r = static_cast<int>(tr);
+  p.tiles = static_cast<int>(tiles);
+  p.nunit = static_cast<int>(std::min<int64_t>(tiles, dev_info().sms / 2));
   p.act = ea.act;
   p.sx = sx;
   p.sw[0] = i8 ? static_cast<const float*>(scales) : nullptr;
@@ -1143,39 +1139,116 @@ aria_status forward_tg(int kind, int64_t M, int64_t N, int64_t K, const void* X,
   p.res = static_cast<const __half*>(ea.res);
   p.save = ea.G != nullptr;
   if ((s = out_map(&pl.m.D[0], Y, M, N)) != ARIA_OK) return s;
-  pl.m.D[1] = pl.m.D[2] = pl.m.D[0];
   if (ea.G && ((s = out_map(&pl.m.D[1], ea.G, M, N)) != ARIA_OK || (s = out_map(&pl.m.D[2], ea.U, M, N)) != ARIA_OK))
     return s;
   const auto dt = i8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   const int es = i8 ? 1 : 2;
-  const int brows = MODE == kTgGated ? p.BN / 2 : p.BN / pl.cg;  // rows of one B box
+  const int brows = p.BN / 2;  // rows of one B box: one CTA's half of the columns
   if ((s = make_map(&pl.m.A[0], X, dt, es, M, K, kelems, kTgRows, CU_TENSOR_MAP_SWIZZLE_128B)) != ARIA_OK) return s;
   if ((s = make_map(&pl.m.B[0], W, dt, es, N, K, kelems, brows, CU_TENSOR_MAP_SWIZZLE_128B)) != ARIA_OK) return s;
-  pl.m.A[1] = pl.m.A[0];
-  pl.m.B[1] = pl.m.B[0];
   if (MODE == kTgGated &&
       (s = make_map(&pl.m.B[1], ea.Wu, dt, es, N, K, kelems, brows, CU_TENSOR_MAP_SWIZZLE_128B)) != ARIA_OK)
     return s;
-  return i8 ? launch_tg<MODE, true, false, false>(pl, st) : launch_tg<MODE, false, false, false>(pl, st);
+  return i8 ? launch_tg<MODE, true>(pl, st) : launch_tg<MODE, false>(pl, st);
 }
 
-// ---- the backward pass's workspace: dG, dU fp16 [M,N], then the column
-// partials fp32 [P][2N], each from a 256-byte boundary
-struct BwdLayout {
+// ---- the backward pass. Workspace: dG, dU fp16 [M,N], the column partials
+// fp32 [P][2N], and where dX's k is split its partials fp32 [S][M][K], each
+// from a 256-byte boundary.
+constexpr int kBwdBn = 256;        // columns of a gradient tile
+constexpr int kBwdMaxParts = 16;
+
+// The longest time of a unit, in K blocks, when `units` pairs take n0 items of
+// length l0 first and then n1 <= l0 long ones; the caps go to *sc.
+int64_t bwd_makespan(int units, int64_t n0, int64_t l0, int64_t n1, int64_t l1, aria::TgSched* sc) {
+  sc->q = static_cast<int>(n0 / units);
+  sc->r = static_cast<int>(n0 % units);
+  const int64_t long_a = (sc->q + 1) * l0, long_b = sc->q * l0;
+  // smallest end time that leaves room for all items of the other type
+  int64_t lo = sc->r ? long_a : long_b, hi = lo + (n1 / units + 1) * l1;
+  auto room = [&](int64_t t) {
+    return sc->r * ((t - long_a) / l1) + static_cast<int64_t>(units - sc->r) * ((t - long_b) / l1);
+  };
+  while (lo < hi) {
+    const int64_t t = lo + (hi - lo) / 2;
+    if (room(t) >= n1) hi = t;
+    else lo = t + 1;
+  }
+  sc->wb = static_cast<int>((lo - long_b) / l1);
+  sc->wa = sc->r ? static_cast<int>((lo - long_a) / l1) : sc->wb;
+  return lo;
+}
+
+struct BwdPlan {
   int rows = 16, P = 1;   // rows per block of the elementwise kernel, blocks along M
-  size_t off_du = 0, off_part = 0, bytes = 0;
+  int parts = 1;          // shares of a dX tile's k
+  int units = 1;
+  aria::TgSched sched{};
 };
 
-BwdLayout bwd_layout(int64_t M, int64_t N) {
-  BwdLayout l;
+BwdPlan bwd_plan(int64_t M, int64_t N, int64_t K, bool dx, bool dw) {
+  using namespace aria;
+  BwdPlan pl;
   // at most 64 partials per column (their sum is read once more), and at
   // least 16 rows per block, one per row lane
-  l.rows = static_cast<int>(std::max<int64_t>(16, ((M + 63) / 64 + 15) / 16 * 16));
-  l.P = static_cast<int>((M + l.rows - 1) / l.rows);
+  pl.rows = static_cast<int>(std::max<int64_t>(16, ((M + 63) / 64 + 15) / 16 * 16));
+  pl.P = static_cast<int>((M + pl.rows - 1) / pl.rows);
+  auto tiles = [](int64_t rows, int64_t cols) {
+    return (rows + 2 * kTgRows - 1) / (2 * kTgRows) * ((cols + kBwdBn - 1) / kBwdBn);
+  };
+  const int units = dev_info().sms / 2;
+  const int64_t tx = dx ? tiles(M, K) : 0, lx = 2 * ((N + 63) / 64);
+  const int64_t tw = dw ? 2 * tiles(N, K) : 0, lw = (M + 63) / 64;
+  // Shares of k for dX: each more than one costs a further launch that reads
+  // the fp32 partials back, about 10 K blocks' time, and every partial is
+  // written and read once more (a K block moves 64 KB per pair in 0.3 us;
+  // all pairs together write and read partials at about 4 TB/s)
+  int64_t best = -1;
+  for (int s = 1; s <= kBwdMaxParts && s <= lx; ++s) {
+    if (s > 1 && (!dx || tx * s > 4 * units)) break;
+    const int64_t l = (lx + s - 1) / s;
+    TgSched sc{};
+    int64_t t;
+    if (l >= lw || !dw) {
+      t = bwd_makespan(units, tx * s, l, tw, lw, &sc);
+      sc.first = 0;
+    } else {
+      t = bwd_makespan(units, tw, lw, tx * s, l, &sc);
+      sc.first = 1;
+    }
+    if (s > 1) t += 10 + s * (M * K * 8 / 4000) / 300;
+    if (best < 0 || t < best) {
+      best = t;
+      sc.n[0] = static_cast<int>(tx * s);
+      sc.n[1] = static_cast<int>(tw);
+      pl.sched = sc;
+      pl.parts = s;
+    }
+  }
+  pl.units = static_cast<int>(std::min<int64_t>(units, std::max<int64_t>(1, tx * pl.parts + tw)));
+  return pl;
+}
+
+// keeps every byte count below 2^48 (no device holds such tensors)
+aria_status check_bwd_size(int64_t M, int64_t N, int64_t K) {
+  constexpr int64_t kMost = int64_t{1} << 40;
+  if (N > kMaxDim / 2) return fail(ARIA_ERR_UNSUPPORTED, "gated: N must be below 2^30");
+  if (M > kMost / N || M > kMost / K || N > kMost / K)
+    return fail(ARIA_ERR_UNSUPPORTED, "gated backward: a tensor of 2^40 elements or more");
+  return ARIA_OK;
+}
+
+struct BwdLayout {
+  size_t off_du = 0, off_part = 0, off_x = 0, bytes = 0;
+};
+
+BwdLayout bwd_layout(int64_t M, int64_t N, int64_t K, int P, int parts) {
+  BwdLayout l;
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   l.off_du = up(static_cast<size_t>(M) * N * 2);
   l.off_part = 2 * l.off_du;
-  l.bytes = l.off_part + up(static_cast<size_t>(l.P) * 2 * N * 4);
+  l.off_x = l.off_part + up(static_cast<size_t>(P) * 2 * N * 4);
+  l.bytes = l.off_x + (parts > 1 ? up(static_cast<size_t>(parts) * M * K * 4) : 0);
   return l;
 }
 
@@ -1244,11 +1317,19 @@ ARIA_API aria_status aria_qgemm_gated(aria_format fmt, int group, int64_t M, int
                                      static_cast<cudaStream_t>(stream), ea);
 }
 
-ARIA_API aria_status aria_gated_bwd_workspace_size(int64_t M, int64_t N, size_t* bytes) {
+ARIA_API aria_status aria_gated_bwd_workspace_size(int64_t M, int64_t N, int64_t K, size_t* bytes) {
   if (!bytes) return fail(ARIA_ERR_INVALID_ARG, "NULL output pointer");
-  if (M < 1 || N < 1 || M > kMaxDim || N > kMaxDim)
-    return fail(ARIA_ERR_INVALID_ARG, "M and N must be in [1, 2^31)");
-  *bytes = bwd_layout(M, N).bytes;
+  if (M < 1 || N < 1 || K < 1 || M > kMaxDim || N > kMaxDim || K > kMaxDim)
+    return fail(ARIA_ERR_INVALID_ARG, "M, N and K must be in [1, 2^31)");
+  aria_status s = check_bwd_size(M, N, K);
+  if (s != ARIA_OK) return s;
+  // enough for every subset of the gradients
+  size_t need = 0;
+  for (int dw = 0; dw < 2; ++dw) {
+    const BwdPlan pl = bwd_plan(M, N, K, true, dw != 0);
+    need = std::max(need, bwd_layout(M, N, K, pl.P, pl.parts).bytes);
+  }
+  *bytes = need;
   return ARIA_OK;
 }
 
@@ -1272,8 +1353,9 @@ ARIA_API aria_status aria_gated_bwd(aria_act act, int64_t M, int64_t N, int64_t 
     return fail(ARIA_ERR_MISALIGNED, "the workspace must be 256-byte aligned");
   aria_status s = check_gemm_shape(M, N, K);
   if (s != ARIA_OK) return s;
-  if (N > kMaxDim / 2) return fail(ARIA_ERR_UNSUPPORTED, "gated: N must be below 2^30");
-  const BwdLayout l = bwd_layout(M, N);
+  if ((s = check_bwd_size(M, N, K)) != ARIA_OK) return s;
+  const BwdPlan bp = bwd_plan(M, N, K, dX != nullptr, dWg != nullptr);
+  const BwdLayout l = bwd_layout(M, N, K, bp.P, bp.parts);
   if (workspace_bytes < l.bytes)
     return fail(ARIA_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes, l.bytes);
   {
@@ -1301,64 +1383,62 @@ ARIA_API aria_status aria_gated_bwd(aria_act act, int64_t M, int64_t N, int64_t 
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
     cfg.stream = st;
-    cfg.gridDim = dim3(static_cast<unsigned>((N + kGbCols - 1) / kGbCols), static_cast<unsigned>(l.P));
+    cfg.gridDim = dim3(static_cast<unsigned>((N + kGbCols - 1) / kGbCols), static_cast<unsigned>(bp.P));
     cfg.blockDim = dim3(kGbThreads);
     set_pdl(cfg, attr);
     cudaError_t e = cudaLaunchKernelEx(&cfg, gated_bwd_kernel, static_cast<const __half*>(dH),
                                        static_cast<const __half*>(G), static_cast<const __half*>(U), dG, dU, part,
-                                       static_cast<int>(M), static_cast<int>(N), l.rows, static_cast<int>(act));
+                                       static_cast<int>(M), static_cast<int>(N), bp.rows, static_cast<int>(act));
     if (e != cudaSuccess) return cuda_fail(e, "gated backward launch");
   }
-  ColSum cs{part, static_cast<__half*>(dbg), static_cast<__half*>(dbu), l.P, static_cast<int>(N)};
-  const int sms = dev_info().sms;
-  if (dX) {
-    // k = 2 N: long, and the output tiles may be few
+  // the column sums are added by idle warps of the products' launch, or, where
+  // a last launch is needed anyway, by that one
+  const bool finish = bp.parts > 1 || (!dX && !dWg);
+  float* xpart = reinterpret_cast<float*>(ws + l.off_x);
+  if (dX || dWg) {
     TgPlan pl;
-    const int64_t nkb = (N + 63) / 64;
-    const int64_t t = ((M + 127) / 128) * ((K + 127) / 128);
-    int splits = 1, bn = 256, cg = 2;
-    if (2 * t <= sms) {
-      bn = 128;
-      cg = 1;
-      splits = static_cast<int>(std::min<int64_t>({kTgMaxSplits, sms / t, 2 * nkb}));
-    } else if (t <= 2 * sms) {
-      bn = 128;
-      cg = 1;
+    if ((s = plan_tg(true, kBwdBn, &pl)) != ARIA_OK) return s;
+    pl.p.sched = bp.sched;
+    pl.p.nunit = bp.units;
+    pl.p.M = static_cast<int>(M);
+    pl.p.N = static_cast<int>(N);
+    pl.p.K = static_cast<int>(K);
+    pl.p.parts = bp.parts;
+    if (part && !finish)
+      pl.p.colsum = ColSum{part, static_cast<__half*>(dbg), static_cast<__half*>(dbu), bp.P, static_cast<int>(N)};
+    if (dX) {
+      if ((s = half_map(&pl.m.A[0], dG, M, N, kTgRows)) != ARIA_OK) return s;
+      if ((s = half_map(&pl.m.A[1], dU, M, N, kTgRows)) != ARIA_OK) return s;
+      if ((s = half_map(&pl.m.B[0], Wg, N, K, 64)) != ARIA_OK) return s;
+      if ((s = half_map(&pl.m.B[1], Wu, N, K, 64)) != ARIA_OK) return s;
+      if ((s = bp.parts > 1 ? partial_map(&pl.m.D[0], xpart, bp.parts, M, K) : out_map(&pl.m.D[0], dX, M, K)) !=
+          ARIA_OK)
+        return s;
     }
-    if ((s = plan_tg(kTgStore, true, cg, bn, splits, M, K, nkb, 2, 1, &pl)) != ARIA_OK) return s;
-    pl.p.D[0] = static_cast<__half*>(dX);
-    if ((s = out_map(&pl.m.D[0], dX, M, K)) != ARIA_OK) return s;
-    pl.m.D[1] = pl.m.D[2] = pl.m.D[0];
-    if (!dWg) pl.p.colsum = cs;
-    if ((s = half_map(&pl.m.A[0], dG, M, N, kTgRows)) != ARIA_OK) return s;
-    if ((s = half_map(&pl.m.A[1], dU, M, N, kTgRows)) != ARIA_OK) return s;
-    if ((s = half_map(&pl.m.B[0], Wg, N, K, 64)) != ARIA_OK) return s;
-    if ((s = half_map(&pl.m.B[1], Wu, N, K, 64)) != ARIA_OK) return s;
-    if ((s = launch_tg<kTgStore, false, false, true>(pl, st)) != ARIA_OK) return s;
+    if (dWg) {
+      if ((s = half_map(&pl.m.A[2], dG, M, N, 64)) != ARIA_OK) return s;
+      if ((s = half_map(&pl.m.A[3], dU, M, N, 64)) != ARIA_OK) return s;
+      if ((s = half_map(&pl.m.B[2], X, M, K, 64)) != ARIA_OK) return s;
+      if ((s = out_map(&pl.m.D[1], dWg, N, K)) != ARIA_OK) return s;
+      if ((s = out_map(&pl.m.D[2], dWu, N, K)) != ARIA_OK) return s;
+    }
+    if ((s = launch_tg<kTgGrad, false>(pl, st)) != ARIA_OK) return s;
   }
-  if (dWg) {
-    TgPlan pl;
-    if ((s = plan_tg(kTgStore, true, 2, 256, 1, N, K, (M + 63) / 64, 1, 2, &pl)) != ARIA_OK) return s;
-    if ((s = out_map(&pl.m.D[0], dWg, N, K)) != ARIA_OK) return s;
-    if ((s = out_map(&pl.m.D[1], dWu, N, K)) != ARIA_OK) return s;
-    pl.m.D[2] = pl.m.D[1];
-    pl.p.colsum = cs;
-    if ((s = half_map(&pl.m.A[0], dG, M, N, 64)) != ARIA_OK) return s;
-    if ((s = half_map(&pl.m.A[1], dU, M, N, 64)) != ARIA_OK) return s;
-    if ((s = half_map(&pl.m.B[0], X, M, K, 64)) != ARIA_OK) return s;
-    pl.m.B[1] = pl.m.B[0];
-    if ((s = launch_tg<kTgStore, false, true, true>(pl, st)) != ARIA_OK) return s;
-  }
-  if (dbg && !dX && !dWg) {
+  if (finish) {
+    const int64_t count = bp.parts > 1 ? M * K : 0;
+    const int64_t nb = part ? (2 * N + 255) / 256 : 0, nx = (count / 4 + 255) / 256;
+    if (nb + nx > kMaxDim) return fail(ARIA_ERR_UNSUPPORTED, "too many elements");
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
     cfg.stream = st;
-    cfg.gridDim = dim3(static_cast<unsigned>((2 * N + 255) / 256));
+    cfg.gridDim = dim3(static_cast<unsigned>(nb + nx));
     cfg.blockDim = dim3(256);
     set_pdl(cfg, attr);
-    cudaError_t e = cudaLaunchKernelEx(&cfg, colsum_kernel, static_cast<const float*>(part), cs.out0, cs.out1,
-                                       cs.P, cs.n);
-    if (e != cudaSuccess) return cuda_fail(e, "column sum launch");
+    cudaError_t e = cudaLaunchKernelEx(&cfg, bwd_finish_kernel, static_cast<const float*>(part),
+                                       static_cast<__half*>(dbg), static_cast<__half*>(dbu), bp.P,
+                                       static_cast<int>(N), static_cast<int>(nb), static_cast<const float*>(xpart),
+                                       static_cast<__half*>(dX), bp.parts, count);
+    if (e != cudaSuccess) return cuda_fail(e, "gated backward's last launch");
   }
   return ARIA_OK;
 }

@@ -37,9 +37,9 @@ __global__ void __launch_bounds__(kGbThreads)
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int c = blockIdx.x * kGbCols + tx * 8;
   const int rb = blockIdx.y * rows, re = rb + min(rows, M - rb);
-  float sg[8], su[8];
+  F2 sg[4], su[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) sg[i] = su[i] = 0.0f;
+  for (int i = 0; i < 4; ++i) sg[i] = su[i] = f2(0.0f);
   if (c < N) {  // N % 16 == 0: 8 columns are wholly in or out
     with_act(act, [&](auto tag) {
       constexpr int kUnroll = 2;
@@ -67,17 +67,15 @@ __global__ void __launch_bounds__(kGbThreads)
           __half2* ou2 = reinterpret_cast<__half2*>(&ou);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float2 h = __half22float2(h2[i]), g = __half22float2(g2[i]), u = __half22float2(u2[i]);
-            float f0, d0, f1, d1;
-            act_fwd_bwd<decltype(tag)::value>(g.x, f0, d0);
-            act_fwd_bwd<decltype(tag)::value>(g.y, f1, d1);
-            const float a0 = h.x * u.x * d0, a1 = h.y * u.y * d1, b0 = h.x * f0, b1 = h.y * f1;
-            sg[2 * i] += a0;
-            sg[2 * i + 1] += a1;
-            su[2 * i] += b0;
-            su[2 * i + 1] += b1;
-            og2[i] = __floats2half2_rn(a0, a1);
-            ou2[i] = __floats2half2_rn(b0, b1);
+            const float2 hv = __half22float2(h2[i]), gv = __half22float2(g2[i]), uv = __half22float2(u2[i]);
+            const F2 h = f2(hv.x, hv.y);
+            F2 fa, da;
+            act_fwd_bwd2<decltype(tag)::value>(f2(gv.x, gv.y), fa, da);
+            const F2 a = f2_mul(f2_mul(h, f2(uv.x, uv.y)), da), b = f2_mul(h, fa);
+            sg[i] = f2_add(sg[i], a);
+            su[i] = f2_add(su[i], b);
+            og2[i] = __float22half2_rn(f2_get(a));
+            ou2[i] = __float22half2_rn(f2_get(b));
           }
           const int64_t o = static_cast<int64_t>(rq) * N + c;
           if (dG) {
@@ -90,9 +88,9 @@ __global__ void __launch_bounds__(kGbThreads)
   }
   if (!part) return;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    red[0][ty][tx * 8 + i] = sg[i];
-    red[1][ty][tx * 8 + i] = su[i];
+  for (int i = 0; i < 4; ++i) {
+    *reinterpret_cast<float2*>(&red[0][ty][tx * 8 + 2 * i]) = f2_get(sg[i]);
+    *reinterpret_cast<float2*>(&red[1][ty][tx * 8 + 2 * i]) = f2_get(su[i]);
   }
   __syncthreads();
   const int half = threadIdx.x >> 7, cc = threadIdx.x & 127;
@@ -105,17 +103,40 @@ __global__ void __launch_bounds__(kGbThreads)
   }
 }
 
-// The column sums alone, when no product follows that could add them.
-__global__ void __launch_bounds__(256) colsum_kernel(const float* __restrict__ part, __half* __restrict__ out0,
-                                                     __half* __restrict__ out1, int P, int n) {
+// The end of a call whose products could not finish everything themselves:
+// the column partials' sums (`part`, P rows of [2 n]; blocks 0 .. nb - 1) and
+// dX from the S fp32 partials [S][count] of its split k (the blocks behind
+// them). Both are added in order.
+__global__ void __launch_bounds__(256)
+    bwd_finish_kernel(const float* __restrict__ part, __half* __restrict__ db0, __half* __restrict__ db1, int P,
+                      int n, int nb, const float* __restrict__ xpart, __half* __restrict__ dX, int S,
+                      int64_t count) {
   pdl_wait();
-  const int c = blockIdx.x * 256 + threadIdx.x;
-  if (c >= 2 * n) return;
-  float s = 0.0f;
+  pdl_launch_dependents();
+  if (static_cast<int>(blockIdx.x) < nb) {
+    const int c = blockIdx.x * 256 + threadIdx.x;
+    if (c >= 2 * n) return;
+    float s = 0.0f;
 #pragma unroll 8
-  for (int i = 0; i < P; ++i) s += ld_dep_f32(part + static_cast<int64_t>(i) * 2 * n + c);
-  if (c < n) out0[c] = __float2half_rn(s);
-  else out1[c - n] = __float2half_rn(s);
+    for (int i = 0; i < P; ++i) s += ld_dep_f32(part + static_cast<int64_t>(i) * 2 * n + c);
+    if (c < n) db0[c] = __float2half_rn(s);
+    else db1[c - n] = __float2half_rn(s);
+    return;
+  }
+  const int64_t e = (static_cast<int64_t>(blockIdx.x - nb) * 256 + threadIdx.x) * 4;  // count % 16 == 0
+  if (e >= count) return;
+  F2 a = f2(0.0f), b = f2(0.0f);
+#pragma unroll 4
+  for (int i = 0; i < S; ++i) {
+    const uint4 v = ld_dep_v4(xpart + static_cast<int64_t>(i) * count + e);
+    a = f2_add(a, f2(__uint_as_float(v.x), __uint_as_float(v.y)));
+    b = f2_add(b, f2(__uint_as_float(v.z), __uint_as_float(v.w)));
+  }
+  uint2 o;
+  __half2* h = reinterpret_cast<__half2*>(&o);
+  h[0] = __float22half2_rn(f2_get(a));
+  h[1] = __float22half2_rn(f2_get(b));
+  *reinterpret_cast<uint2*>(dX + e) = o;
 }
 
 }  // namespace aria

@@ -1,5 +1,5 @@
 // tgemm.cuh -- token-major GEMM on the tensor cores (tcgen05): the
-// feed-forward operators over many tokens, forward and backward.
+// feed-forward operators over many tokens, and their gradients.
 //
 //   D[r, c] = sum over k of A[r, k] * B[c, k]
 //
@@ -9,31 +9,38 @@
 //
 //   forward     rows = tokens,   columns = channels, k = input features
 //               A = X K-major, B = W K-major; gated: the columns of a tile are
-//               BN/2 gate channels and the BN/2 up channels beside them, so
+//               128 gate channels and the 128 up channels beside them, so
 //               one thread holds both pre-activations of its outputs
 //   dX          rows = tokens,   columns = input features, k = channels, of
 //               the gate and then of the up projection (two sources)
 //               A = dG, dU K-major, B = Wg, Wu MN-major
 //   dWg, dWu    rows = channels, columns = input features, k = tokens
-//               A = dG, dU MN-major, B = X MN-major (two problems)
+//               A = dG, dU MN-major, B = X MN-major
 //
 // Beside qgemm.cuh, whose tiles have the weight channels as MMA rows: here
-// the rows are the tile's 128 (or, over a CTA pair, 256) tokens. The
-// epilogue then needs no transpose, and a pair of CTAs shares one
-// 256 x BN tile (cta_group::2), each holding half of B: a K block moves 32 KB
-// through each SM's shared memory for 128 x 256 x 64 products, where one
-// CTA alone moves 48 KB. The tensor core reads shared memory at 128 bytes
-// per cycle, which is what bounds the single-CTA form.
+// the rows are tokens (or, for dW, channels), and a pair of CTAs shares one
+// 256-row tile (cta_group::2), each holding its 128 rows of A and half of B.
+// A K block then moves 32 KB into each SM for 128 x 256 x 64 products where a
+// lone CTA moves 48 KB, and shared memory, which the tensor core reads at 128
+// bytes per cycle, keeps up with it: fp16 at M = 8192, N = K = 8192 ran at
+// 1390 TFLOP/s with its epilogue taken out and 1240-1280 with it, cuBLAS at
+// 1373 (both under the power cap). Loads alone took 295 ns per K block, the
+// MMAs alone 300, both 350 (at 1.3 tiles per pair) to 480 (power-capped).
 //
 // Roles of a CTA (12 warps): warp 0 TMA producer, warp 1 TMEM allocation and
 // MMA issue (the pair's first CTA issues for both), warps 2 and 3 the column
 // sums that a backward call still has to add up (see ColSum), warps 4..11
 // epilogue. Two accumulators of up to 256 columns in TMEM: a tile's epilogue
-// overlaps the next tile's mainloop. Every wait is bounded.
+// overlaps the next tile's mainloop. The epilogue works on packed fp32 pairs
+// and writes through small swizzled boxes that leave by TMA; with scalar
+// arithmetic and 16-byte stores per row it was what bounded the forward
+// operators (M = 4096, N = 6144, K = 1536: gated fp16 with its
+// pre-activations 136 against 121 us, gated W8A8 77-86 against 62, fp16 with
+// GELU 75 against 67). Every wait is bounded.
 //
-// Few tiles (a gradient dX over few tokens, whose k is long): CG = 1 and a
-// cluster of S CTAs divides k; the partial tiles meet in shared memory and
-// are added in rank order (deterministic, no atomics, no global scratch).
+// The two gradients run in ONE launch, over one list of work items: dX tiles
+// have a long k (2 N), dW tiles a short one (M), and the pairs take the long
+// ones first and fill up with the short ones (see TgSched).
 #pragma once
 
 #include <cuda_fp16.h>
@@ -44,22 +51,21 @@
 
 namespace aria {
 
-enum TgMode : int { kTgStore = 0, kTgAct = 1, kTgGated = 2 };
+enum TgMode : int { kTgGrad = 0, kTgAct = 1, kTgGated = 2 };
 
 constexpr int kTgThreads = 384;
 constexpr int kTgEpiWarps = 8;
-constexpr int kTgRows = 128;              // rows per CTA
+constexpr int kTgRows = 128;              // rows per CTA; a pair's tile has twice as many
 constexpr uint32_t kTgATile = 16384;      // 128 rows x 64 fp16 (or 128 int8) of k
 constexpr uint32_t kTgAccCols = 256;
-constexpr int kTgMaxSplits = 8;
-
 constexpr uint32_t kTgBox = 32 * 64;      // output box of a warp: 32 rows x 32 fp16
-constexpr int kTgSlots = 2;               // store boxes per epilogue warp
+constexpr int kTgSlots = 2;               // store boxes per epilogue warp (both together: 32 x 32 fp32)
 constexpr uint32_t kTgStageBytes = kTgEpiWarps * kTgSlots * kTgBox;
 
 struct TgMaps {
-  CUtensorMap A[2], B[2];
-  CUtensorMap D[3];  // outputs: one per problem; gated: H, G, U
+  CUtensorMap A[4];  // forward: X; gradients: dG, dU as rows of tokens, then as rows of channels
+  CUtensorMap B[3];  // forward: W (gated: gate, up); gradients: Wg, Wu, X
+  CUtensorMap D[3];  // forward: Y or H, G, U; gradients: dX (split k: its fp32 partials), dWg, dWu
 };
 
 // Column sums left over from an earlier kernel of the call: P rows of fp32
@@ -71,16 +77,30 @@ struct ColSum {
   int P, n;
 };
 
+// Work items of a gradient launch. An item of type 0 is one of `parts` equal
+// shares of the k of a dX tile, an item of type 1 a dW tile. Units (pairs)
+// 0 .. r - 1 take q + 1 items of the longer type, the others q; then every
+// unit takes items of the other type up to a cap chosen by the host so that
+// all end at about the same time: wa for the first r units, wb >= wa for the
+// others.
+struct TgSched {
+  int first;              // the longer type
+  int n[2];               // items of either type
+  int q, r, wa, wb;
+};
+
 struct TgParams {
-  int R, C;                // output rows and columns of one problem
-  int nkb;                 // K blocks (128 bytes of k) of one source
-  int nsrc;                // sources summed into one output
+  int R, C;                // forward: output rows and columns
+  int nkb;                 // forward: K blocks (128 bytes of k)
   int BN;                  // accumulator columns per tile (gated: 2 x channels)
-  int tiles_r, tiles_c, tiles;  // tiles: over all problems (tiles_r per problem)
-  int nstage, splits;
+  int tiles_r, tiles, nunit;
+  int nstage;
   uint32_t b_stage;        // bytes of this CTA's part of a B tile
   uint32_t off_a, off_b, off_out, off_col, off_bar;
-  // epilogue
+  // gradients
+  TgSched sched;
+  int M, N, K, parts;      // tokens, channels, input features; shares of a dX tile's k
+  // forward epilogue
   int act;
   const float* sx;         // int8: token scales [R]
   const float* sw[2];      // int8: channel scales (gated: gate, up)
@@ -88,8 +108,7 @@ struct TgParams {
   const float* steer;      // kTgAct
   float alpha;
   const float* alpha_dev;
-  const __half* res;       // kTgAct: [R,C] or null; may be D itself
-  __half* D[2];            // split-K: outputs, one per problem
+  const __half* res;       // kTgAct: [R,C] or null; may be Y itself
   int save;                // kTgGated: keep the pre-activations
   ColSum colsum;
 };
@@ -107,68 +126,51 @@ __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t smem_addr) {
   return d;
 }
 
-template <int CG, bool I8>
+template <bool I8>
 __device__ __forceinline__ void tg_mma(uint32_t d_tmem, uint64_t ad, uint64_t bd, uint32_t idesc,
                                        uint32_t accumulate) {
-#define ARIA_TG_MMA(group, kind)                                                   \
-  asm volatile(                                                                    \
-      "{\n\t.reg .pred e, p;\n\t"                                                  \
-      "elect.sync _|e, 0xffffffff;\n\t"                                            \
-      "setp.ne.b32 p, %4, 0;\n\t"                                                  \
-      "@e tcgen05.mma.cta_group::" group ".kind::" kind " [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem), \
-      "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate)                                \
-      : "memory")
-  if constexpr (CG == 2) {
-    if constexpr (I8) ARIA_TG_MMA("2", "i8");
-    else ARIA_TG_MMA("2", "f16");
-  } else {
-    if constexpr (I8) ARIA_TG_MMA("1", "i8");
-    else ARIA_TG_MMA("1", "f16");
-  }
-#undef ARIA_TG_MMA
-}
-
-// the completion of all MMAs issued so far arrives on this barrier, in both
-// CTAs of a pair
-template <int CG>
-__device__ __forceinline__ void tg_commit(uint64_t* bar) {
-  if constexpr (CG == 2) {
+  if constexpr (I8)
     asm volatile(
-        "{\n\t.reg .pred e;\n\t.reg .b16 m;\n\t"
-        "mov.b16 m, 3;\n\t"
+        "{\n\t.reg .pred e, p;\n\t"
         "elect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::
-            "r"(smem_u32(bar))
-        : "memory");
-  } else {
-    umma_commit_elect(bar);
-  }
-}
-
-// a CTA of a pair loads its own part of a tile and reports to the pair's
-// first CTA (`bar`: that CTA's barrier as a cluster address)
-template <int CG>
-__device__ __forceinline__ void tg_load(const CUtensorMap* m, uint32_t bar, void* dst, int32_t x, int32_t y) {
-  if constexpr (CG == 2)
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y)
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate)
         : "memory");
   else
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y)
+        "{\n\t.reg .pred e, p;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+
+// the completion of all MMAs issued so far arrives on this barrier of both
+// CTAs
+__device__ __forceinline__ void tg_commit(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t.reg .b16 m;\n\t"
+      "mov.b16 m, 3;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::
+          "r"(smem_u32(bar))
+      : "memory");
+}
+
+// a CTA loads its own part of a tile into its own shared memory and reports
+// to the pair's first CTA (`bar`: that CTA's barrier as a cluster address)
+__device__ __forceinline__ void tg_load(const CUtensorMap* m, uint32_t bar, void* dst, int32_t x, int32_t y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y)
+      : "memory");
 }
 
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
-}
-
-__device__ __forceinline__ void st_dsmem_wait_visible() {
-  asm volatile("fence.acq_rel.cluster;" ::: "memory");
 }
 
 // 32 results of this lane's row -> its 64 bytes of the warp's store box
@@ -206,8 +208,24 @@ __device__ __forceinline__ void tg_pre(const uint32_t (&v)[32], float sx, const 
   }
 }
 
-// CG: CTAs sharing a tile (1 or 2). AMN, BMN: operand MN-major.
-template <int MODE, bool I8, int CG, bool AMN, bool BMN>
+// 32 accumulators of this lane's row -> its 128 bytes of a 32 x 32 fp32 box
+// (128-byte swizzle)
+__device__ __forceinline__ void tg_box_row_f32(uint8_t* box, int lane, const uint32_t (&v)[32]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    *reinterpret_cast<uint4*>(box + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+        make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+}
+
+// One work item as a CTA of a pair sees it.
+struct TgItem {
+  int type;        // gradients: 0 = dX, 1 = dW
+  int src;         // dW: 0 = gate, 1 = up; dX: the share of k
+  int r0, c0;      // this CTA's first row; the tile's first column
+  int kb0, kb1;    // K blocks
+};
+
+template <int MODE, bool I8>
 __global__ void __launch_bounds__(kTgThreads, 1)
     tgemm_kernel(const __grid_constant__ TgMaps tm, const TgParams p) {
   extern __shared__ uint8_t dyn_smem[];
@@ -216,18 +234,13 @@ __global__ void __launch_bounds__(kTgThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kKElems = I8 ? 128 : 64;  // k per 128-byte block
 
-  const bool split = CG == 1 && p.splits > 1;
-  const int rank = (CG == 2 || split) ? static_cast<int>(cluster_ctarank()) : 0;
-  const int crank = CG == 2 ? rank : 0;                        // place in the pair
-  const int unit = static_cast<int>(blockIdx.x) / (split ? p.splits : CG);
-  const int nunit = static_cast<int>(gridDim.x) / (split ? p.splits : CG);
-  const int kb_all = p.nkb * p.nsrc;
-  const int kb0 = split ? static_cast<int>(static_cast<int64_t>(kb_all) * rank / p.splits) : 0;
-  const int kb1 = split ? static_cast<int>(static_cast<int64_t>(kb_all) * (rank + 1) / p.splits) : kb_all;
+  const int crank = static_cast<int>(cluster_ctarank());  // place in the pair
+  const int unit = static_cast<int>(blockIdx.x) >> 1;
+  const int chans = MODE == kTgGated ? p.BN / 2 : p.BN;   // output columns per tile
 
   uint8_t* abuf = smem + p.off_a;
   uint8_t* bbuf = smem + p.off_b;
-  float* col = reinterpret_cast<float*>(smem + p.off_col);  // [2 tiles][3][kTgAccCols]
+  float* col = reinterpret_cast<float*>(smem + p.off_col);  // forward: [2 tiles][3][kTgAccCols]
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + p.off_bar);
   uint64_t* empty = full + p.nstage;
   uint64_t* acc_full = empty + p.nstage;   // [2]
@@ -243,89 +256,124 @@ __global__ void __launch_bounds__(kTgThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(acc_full + i, 1);
-      mbar_init(acc_empty + i, CG * kTgEpiWarps);
+      mbar_init(acc_empty + i, 2 * kTgEpiWarps);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
-    for (int i = 0; i < 2; ++i) {
-      prefetch_tmap(&tm.A[i]);
-      prefetch_tmap(&tm.B[i]);
+    if constexpr (MODE != kTgGrad) {  // (a gradient launch fills only the maps that it uses)
+      prefetch_tmap(&tm.A[0]);
+      prefetch_tmap(&tm.B[0]);
+      prefetch_tmap(&tm.D[0]);
     }
   }
   if (warp == 1) {
-    if constexpr (CG == 2) {
-      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
-                   "r"(2 * kTgAccCols)
-                   : "memory");
-      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-    } else {
-      tmem_alloc(tmem_slot, 2 * kTgAccCols);
-      tmem_relinquish();
-    }
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(2 * kTgAccCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   tc_fence_before();
   __syncthreads();
-  if constexpr (CG == 2) cluster_sync();  // the peer's barriers are initialised
+  cluster_sync();  // the peer's barriers are initialised
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   pdl_wait();
   pdl_launch_dependents();
 
-  // tile -> problem, row tile (fastest: neighbours share B), column tile
-  auto tile_at = [&](int t, int& prob, int& r0, int& tc) {
-    const int per = p.tiles_r * p.tiles_c;
-    prob = t / per;
-    const int q = t % per;
-    r0 = (q % p.tiles_r) * (kTgRows * CG) + crank * kTgRows;
-    tc = q / p.tiles_r;
+  // The unit's i-th item; false behind its last one. Neighbouring units take
+  // neighbouring items at the same time, so their operands meet in L2.
+  auto item_at = [&](int i, TgItem& it) -> bool {
+    int idx;
+    if constexpr (MODE == kTgGrad) {
+      const TgSched& sc = p.sched;
+      const int nl = sc.q + (unit < sc.r);  // items of the longer type
+      if (i < nl) {
+        it.type = sc.first;
+        idx = i * p.nunit + unit;
+      } else {
+        it.type = sc.first ^ 1;
+        const int j = i - nl;
+        if (j < sc.wa) {
+          idx = j * p.nunit + unit;
+        } else {
+          if (unit < sc.r || j >= sc.wb) return false;
+          idx = sc.wa * p.nunit + (j - sc.wa) * (p.nunit - sc.r) + (unit - sc.r);
+        }
+      }
+      if (idx >= sc.n[it.type]) return false;
+      const int tiles_c = (p.K + p.BN - 1) / p.BN;
+      if (it.type == 0) {
+        const int kb_all = 2 * ((p.N + 63) / 64);
+        const int tile = idx / p.parts;
+        it.src = idx - tile * p.parts;
+        it.kb0 = static_cast<int>(static_cast<int64_t>(kb_all) * it.src / p.parts);
+        it.kb1 = static_cast<int>(static_cast<int64_t>(kb_all) * (it.src + 1) / p.parts);
+        it.r0 = (tile / tiles_c) * (2 * kTgRows);
+        it.c0 = (tile % tiles_c) * p.BN;
+      } else {
+        const int per = sc.n[1] / 2;  // tiles of one projection
+        it.src = idx >= per;
+        const int tile = idx - it.src * per;
+        it.kb0 = 0;
+        it.kb1 = (p.M + 63) / 64;
+        it.r0 = (tile / tiles_c) * (2 * kTgRows);
+        it.c0 = (tile % tiles_c) * p.BN;
+      }
+    } else {
+      idx = i * p.nunit + unit;
+      if (idx >= p.tiles) return false;
+      it.type = it.src = 0;
+      it.r0 = (idx % p.tiles_r) * (2 * kTgRows);
+      it.c0 = (idx / p.tiles_r) * chans;
+      it.kb0 = 0;
+      it.kb1 = p.nkb;
+    }
+    it.r0 += crank * kTgRows;
+    return true;
   };
 
   int issued = 0;
   if (warp == 0) {
     // ------------------------------------------------------ TMA producer
-    const uint32_t full0 = CG == 2 ? mapa_shared(smem_u32(full), 0) : smem_u32(full);
-    const uint32_t tx = CG * (kTgATile + p.b_stage);
-    const int bn_cta = p.BN / CG;  // this CTA's columns of B
+    const uint32_t full0 = mapa_shared(smem_u32(full), 0);
+    const uint32_t tx = 2 * (kTgATile + p.b_stage);  // both CTAs' bytes
+    const int bn_cta = p.BN / 2;                     // this CTA's columns of B
     int s = 0;
     uint32_t ph = 0;
     bool ok = true;
-    for (int t = unit; t < p.tiles && ok; t += nunit) {
-      int prob, r0, tc;
-      tile_at(t, prob, r0, tc);
-      for (int kb = kb0; kb < kb1; ++kb) {
+    TgItem it;
+    for (int i = 0; ok && item_at(i, it); ++i) {
+      for (int kb = it.kb0; kb < it.kb1; ++kb) {
         if (!(ok = mbar_wait_warp(empty + s, ph ^ 1, abort_flag, 40))) break;
         if (lane == 0) {
-          const int src = kb / p.nkb, x = (kb - src * p.nkb) * kKElems;
           if (crank == 0) mbar_arrive_expect_tx(full + s, tx);
           const uint32_t bar = full0 + static_cast<uint32_t>(s) * 8u;
           uint8_t* a = abuf + s * kTgATile;
           uint8_t* b = bbuf + s * p.b_stage;
-          const CUtensorMap* ma = &tm.A[p.nsrc == 2 ? src : prob];
-          if constexpr (AMN) {
-            tg_load<CG>(ma, bar, a, r0, x);
-            tg_load<CG>(ma, bar, a + 8192, r0 + 64, x);
-          } else {
-            tg_load<CG>(ma, bar, a, x, r0);
-          }
-          if constexpr (MODE == kTgGated) {
-            // CTA pair: the first CTA brings the gate's channels, the second
-            // the up projection's; a lone CTA brings both
-            const int c0 = tc * (p.BN / 2);
-            if constexpr (CG == 2) {
-              tg_load<CG>(&tm.B[crank], bar, b, x, c0);
+          if constexpr (MODE == kTgGrad) {
+            const CUtensorMap* mb;
+            int x;
+            if (it.type == 0) {
+              const int nkb = (p.N + 63) / 64, src = kb >= nkb;
+              x = (kb - src * nkb) * 64;
+              tg_load(&tm.A[src], bar, a, x, it.r0);
+              mb = &tm.B[src];
             } else {
-              tg_load<CG>(&tm.B[0], bar, b, x, c0);
-              tg_load<CG>(&tm.B[1], bar, b + (p.b_stage >> 1), x, c0);
+              x = kb * 64;
+              tg_load(&tm.A[2 + it.src], bar, a, it.r0, x);
+              tg_load(&tm.A[2 + it.src], bar, a + 8192, it.r0 + 64, x);
+              mb = &tm.B[2];
             }
+            const int c = it.c0 + crank * bn_cta;
+            for (int j = 0; j < bn_cta; j += 64) tg_load(mb, bar, b + j * 128, c + j, x);
           } else {
-            const int c0 = tc * p.BN + crank * bn_cta;
-            const CUtensorMap* mb = &tm.B[p.nsrc == 2 ? src : 0];
-            if constexpr (BMN) {
-              for (int j = 0; j < bn_cta; j += 64) tg_load<CG>(mb, bar, b + j * 128, c0 + j, x);
-            } else {
-              tg_load<CG>(mb, bar, b, x, c0);
-            }
+            const int x = kb * kKElems;
+            tg_load(&tm.A[0], bar, a, x, it.r0);
+            // gated: the first CTA brings the gate's channels, the second
+            // the up projection's
+            if constexpr (MODE == kTgGated) tg_load(&tm.B[crank], bar, b, x, it.c0);
+            else tg_load(&tm.B[0], bar, b, x, it.c0 + crank * bn_cta);
           }
         }
         ++issued;
@@ -335,39 +383,43 @@ __global__ void __launch_bounds__(kTgThreads, 1)
   } else if (warp == 1) {
     // --------------------------------------------------------- MMA issuer
     if (crank == 0) {
-      uint32_t idesc = I8 ? idesc_s8_s32(p.BN) : idesc_f16_f32(p.BN);
-      if (CG == 2) idesc += (128u >> 4) << 24;  // M = 256
-      if (AMN) idesc |= 1u << 15;
-      if (BMN) idesc |= 1u << 16;
-      int ti = 0, s = 0;
+      // M = 256
+      const uint32_t idesc0 = (I8 ? idesc_s8_s32(p.BN) : idesc_f16_f32(p.BN)) + ((128u >> 4) << 24);
+      int s = 0;
       uint32_t ph = 0;
       bool ok = true;
-      for (int t = unit; t < p.tiles && ok; t += nunit, ++ti) {
-        const int b = ti & 1;
-        if (!(ok = mbar_wait_warp(acc_empty + b, ((ti >> 1) & 1) ^ 1, abort_flag, 41))) break;
-        if constexpr (CG == 2) st_dsmem_wait_visible();  // the peer's arrivals
+      TgItem it;
+      for (int i = 0; ok && item_at(i, it); ++i) {
+        const int b = i & 1;
+        if (!(ok = mbar_wait_warp(acc_empty + b, ((i >> 1) & 1) ^ 1, abort_flag, 41))) break;
+        asm volatile("fence.acq_rel.cluster;" ::: "memory");  // the peer's arrivals
         tc_fence_after();
         const uint32_t dt = tmem_base + b * kTgAccCols;
-        for (int kb = kb0; kb < kb1; ++kb) {
+        // MN-major operands: bits 15 (A) and 16 (B)
+        const bool amn = MODE == kTgGrad && it.type == 1;
+        constexpr bool bmn = MODE == kTgGrad;
+        const uint32_t idesc = idesc0 | (amn ? 1u << 15 : 0u) | (bmn ? 1u << 16 : 0u);
+        const uint32_t astep = amn ? 128 : 2;  // K-major: 32 bytes per 16 k; MN-major: 16 rows of 128 bytes
+        for (int kb = it.kb0; kb < it.kb1; ++kb) {
           if (!(ok = mbar_wait_warp(full + s, ph, abort_flag, 42))) break;
           tc_fence_after();
           const uint32_t a_u = smem_u32(abuf + s * kTgATile), b_u = smem_u32(bbuf + s * p.b_stage);
-          const uint64_t ad = AMN ? sdesc_mn_sw128(a_u) : sdesc_sw128(a_u);
-          const uint64_t bd = BMN ? sdesc_mn_sw128(b_u) : sdesc_sw128(b_u);
+          const uint64_t ad = amn ? sdesc_mn_sw128(a_u) : sdesc_sw128(a_u);
+          const uint64_t bd = bmn ? sdesc_mn_sw128(b_u) : sdesc_sw128(b_u);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)  // K-major: 32 bytes per step; MN-major: 16 rows of 128 bytes
-            tg_mma<CG, I8>(dt, ad + (AMN ? 128 : 2) * j, bd + (BMN ? 128 : 2) * j, idesc, (kb > kb0) | (j > 0));
-          tg_commit<CG>(empty + s);
+          for (int j = 0; j < 4; ++j)
+            tg_mma<I8>(dt, ad + astep * j, bd + (bmn ? 128 : 2) * j, idesc, (kb > it.kb0) | (j > 0));
+          tg_commit(empty + s);
           if (++s == p.nstage) { s = 0; ph ^= 1u; }
         }
-        tg_commit<CG>(acc_full + b);
+        tg_commit(acc_full + b);
       }
     }
   } else if (warp < 4) {
     // --------------------------------- column sums of an earlier kernel
     // One thread per output, the partials in order; their loads are
     // independent, so eight are in flight.
-    if (MODE == kTgStore && p.colsum.part) {
+    if (MODE == kTgGrad && p.colsum.part) {
       const ColSum& cs = p.colsum;
       const int n2 = 2 * cs.n;
       for (int c = static_cast<int>(blockIdx.x) * 64 + (warp - 2) * 32 + lane; c < n2;
@@ -380,53 +432,53 @@ __global__ void __launch_bounds__(kTgThreads, 1)
         else cs.out1[c - cs.n] = h;
       }
     }
-  } else if (!split) {
+  } else {
     // ----------------------------------------------------------- epilogue
     const int e = warp - 4, te = threadIdx.x - 128;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const int cg = e >> 2;  // this warp takes chunks cg, cg + 2, ...
-    const int chans = MODE == kTgGated ? p.BN / 2 : p.BN;
-    const uint32_t release0 = CG == 2 ? mapa_shared(smem_u32(acc_empty), 0) : smem_u32(acc_empty);
+    const int cg = e >> 2;  // this warp takes 32-column units cg, cg + 2, ...
+    const uint32_t release0 = mapa_shared(smem_u32(acc_empty), 0);
     const float alpha = (MODE == kTgAct && p.steer) ? (p.alpha_dev ? *p.alpha_dev : p.alpha) : 0.0f;
-    // column constants of a tile, one tile ahead: bias, scale, steering
-    auto col_load = [&](int t, float (&cv)[3]) {
+    // column constants of an item, one item ahead: bias, scale, steering
+    auto col_load = [&](bool valid, const TgItem& it, float (&cv)[3]) {
       cv[0] = cv[2] = 0.0f;
       cv[1] = 1.0f;
-      if constexpr (MODE == kTgStore) return;
-      if (t >= p.tiles || te >= p.BN) return;
-      int prob, r0, tc;
-      tile_at(t, prob, r0, tc);
+      if (!valid || te >= p.BN) return;
       const bool up = MODE == kTgGated && te >= chans;
-      const int c = tc * chans + (up ? te - chans : te);
+      const int c = it.c0 + (up ? te - chans : te);
       if (c >= p.C) return;
       const __half* bp = up ? p.bias[1] : p.bias[0];
       if (bp) cv[0] = __half2float(__ushort_as_half(ld_dep_u16(bp + c)));
       if constexpr (I8) cv[1] = ld_dep_f32((up ? p.sw[1] : p.sw[0]) + c);
       if (MODE == kTgAct && alpha != 0.0f) cv[2] = alpha * ld_dep_f32(p.steer + c);
     };
-    float cv[3];
-    col_load(unit, cv);
     uint8_t* boxes = smem + p.off_out + e * (kTgSlots * kTgBox);
-    int ti = 0, nst = 0;
-    for (int t = unit; t < p.tiles; t += nunit, ++ti) {
-      const int b = ti & 1;
-      int prob, r0, tc;
-      tile_at(t, prob, r0, tc);
+    float cv[3];
+    TgItem it, nx;
+    bool valid = item_at(0, nx);
+    if constexpr (MODE != kTgGrad) col_load(valid, nx, cv);
+    int nst = 0;
+    for (int i = 0; valid; ++i) {
+      it = nx;
+      valid = item_at(i + 1, nx);
+      const int b = i & 1;
       float* cb = col + b * 3 * kTgAccCols;
-      if constexpr (MODE != kTgStore) {
+      if constexpr (MODE != kTgGrad) {
 #pragma unroll
         for (int k = 0; k < 3; ++k) cb[k * kTgAccCols + te] = cv[k];
-        named_bar(1, kTgEpiWarps * 32);  // and every reader of this buffer two tiles ago is done
-        col_load(t + nunit, cv);
+        named_bar(1, kTgEpiWarps * 32);  // and every reader of this buffer two items ago is done
+        col_load(valid, nx, cv);
       }
-      const int rw = r0 + (warp & 3) * 32, r = rw + lane;  // this warp's first row, this lane's row
-      const bool row_in = r < p.R;
-      const int64_t ro = static_cast<int64_t>(r) * p.C;
+      const int rw = it.r0 + (warp & 3) * 32, r = rw + lane;  // this warp's first row, this lane's row
+      const int rows = MODE == kTgGrad ? (it.type == 0 ? p.M : p.N) : p.R;
+      const int cols = MODE == kTgGrad ? p.K : p.C;
+      const bool row_in = r < rows;
+      const int64_t ro = static_cast<int64_t>(r) * cols;
       float sx = 1.0f;
       if constexpr (I8) sx = row_in ? ld_dep_f32(p.sx + r) : 0.0f;
-      bool ok = mbar_wait(acc_full + b, (ti >> 1) & 1, abort_flag, 43);
+      bool ok = mbar_wait(acc_full + b, (i >> 1) & 1, abort_flag, 43);
       ok = __all_sync(0xffffffffu, ok);
-      if (!ok) continue;  // (stays with the named barriers of later tiles)
+      if (!ok) continue;  // (stays with the named barriers of later items)
       tc_fence_after();
       const uint32_t tacc = tmem_base + lane_off + b * kTgAccCols;
       // units of 32 columns; a result goes through a store box of the warp's
@@ -440,22 +492,35 @@ __global__ void __launch_bounds__(kTgThreads, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          if (rw < p.R) tma_store_2d(m, box, c0, rw);
+          if (rw < rows) tma_store_2d(m, box, c0, rw);
           bulk_commit();
         }
       };
       const int nunit32 = (chans + 31) / 32;
       for (int c = cg; c < nunit32; c += 2) {
-        const int c0 = tc * chans + c * 32;
-        if (c0 >= p.C) break;
+        const int c0 = it.c0 + c * 32;
+        if (c0 >= cols) break;
         uint32_t v[32];
         tmem_ld32(tacc + c * 32, v);
         F2 z[16];
-        if constexpr (MODE == kTgStore) {
+        if constexpr (MODE == kTgGrad) {
           tmem_ld_wait();
+          if (it.type == 0 && p.parts > 1) {
+            // a share of k: fp32, through both boxes
+            if (lane == 0) bulk_wait_read<0>();
+            __syncwarp();
+            tg_box_row_f32(boxes, lane, v);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (rw < rows) tma_store_3d(&tm.D[0], boxes, c0, rw, it.src);
+              bulk_commit();
+            }
+          } else {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) z[i] = f2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-          box_store(&tm.D[prob], z, c0);
+            for (int j = 0; j < 16; ++j) z[j] = f2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+            box_store(&tm.D[it.type == 0 ? 0 : 1 + it.src], z, c0);
+          }
         } else if constexpr (MODE == kTgAct) {
           uint4 rv[4];
 #pragma unroll
@@ -467,7 +532,7 @@ __global__ void __launch_bounds__(kTgThreads, 1)
           tg_pre<I8>(v, sx, cb + kTgAccCols + c * 32, cb + c * 32, z);
           with_act(p.act, [&](auto tag) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) z[i] = act_fwd2<decltype(tag)::value>(z[i]);
+            for (int j = 0; j < 16; ++j) z[j] = act_fwd2<decltype(tag)::value>(z[j]);
           });
           if (alpha != 0.0f) {
 #pragma unroll
@@ -480,9 +545,9 @@ __global__ void __launch_bounds__(kTgThreads, 1)
           if (p.res) {
             const __half2* hr = reinterpret_cast<const __half2*>(rv);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float2 f = __half22float2(hr[i]);
-              z[i] = f2_add(z[i], f2(f.x, f.y));
+            for (int j = 0; j < 16; ++j) {
+              const float2 f = __half22float2(hr[j]);
+              z[j] = f2_add(z[j], f2(f.x, f.y));
             }
           }
           box_store(&tm.D[0], z, c0);
@@ -499,86 +564,20 @@ __global__ void __launch_bounds__(kTgThreads, 1)
           }
           with_act(p.act, [&](auto tag) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) z[i] = f2_mul(act_fwd2<decltype(tag)::value>(z[i]), u[i]);
+            for (int j = 0; j < 16; ++j) z[j] = f2_mul(act_fwd2<decltype(tag)::value>(z[j]), u[j]);
           });
           box_store(&tm.D[0], z, c0);
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        if constexpr (CG == 2) mbar_arrive_cluster(release0 + b * 8u);
-        else mbar_arrive(acc_empty + b);
-      }
+      if (lane == 0) mbar_arrive_cluster(release0 + b * 8u);
     }
     if (lane == 0) bulk_wait_all();
   }
 
-  // -------------------------------------------- split-K: cluster reduction
-  // One tile per cluster. The partial tile goes to shared memory as fp32
-  // rows of BN + 4 words (the pad spreads a warp's 16-byte stores, one row
-  // per lane, over the banks); after a cluster barrier rank q adds rows
-  // [128 q / S, 128 (q + 1) / S) in rank order and stores them.
-  if (split) {
-    const bool ok = mbar_wait_warp(acc_full, 0, abort_flag, 44);
-    float* red = reinterpret_cast<float*>(smem);
-    const uint32_t stride = static_cast<uint32_t>(p.BN) + 4u;
-    tc_fence_after();
-    {
-      const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-      float* rr = red + ((warp & 3) * 32 + lane) * stride;
-      for (int c = warp >> 2; c < p.BN / 16; c += 3) {
-        uint32_t v[16];
-        tmem_ld16(tmem_base + lane_off + c * 16, v);
-        tmem_ld_wait();
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          *reinterpret_cast<uint4*>(rr + c * 16 + 4 * q) =
-              ok ? make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]) : make_uint4(0u, 0u, 0u, 0u);
-      }
-    }
-    __syncwarp();
-    cluster_sync();
-    int prob, r0, tc;
-    tile_at(unit, prob, r0, tc);
-    const int rb = kTgRows * rank / p.splits, re = kTgRows * (rank + 1) / p.splits;
-    const int per_row = p.BN / 8;  // 8 columns per thread
-    const uint32_t red_u32 = smem_u32(smem);
-    for (int i = threadIdx.x; i < (re - rb) * per_row; i += kTgThreads) {
-      const int row = rb + i / per_row, c8 = (i % per_row) * 8;
-      const int r = r0 + row, c = tc * p.BN + c8;
-      if (r >= p.R || c >= p.C) continue;  // C % 16 == 0
-      uint4 a[kTgMaxSplits][2];
-#pragma unroll
-      for (int q = 0; q < kTgMaxSplits; ++q) {
-        if (q < p.splits) {
-          const uint32_t ad = mapa_shared(red_u32 + (row * stride + c8) * 4u, q);
-          a[q][0] = ld_dsmem_v4(ad);
-          a[q][1] = ld_dsmem_v4(ad + 16u);
-        }
-      }
-      float y[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) y[k] = 0.0f;
-#pragma unroll
-      for (int q = 0; q < kTgMaxSplits; ++q) {
-        if (q < p.splits) {
-          const uint32_t w[8] = {a[q][0].x, a[q][0].y, a[q][0].z, a[q][0].w, a[q][1].x, a[q][1].y, a[q][1].z, a[q][1].w};
-#pragma unroll
-          for (int k = 0; k < 8; ++k) y[k] += __uint_as_float(w[k]);
-        }
-      }
-      uint4 o;
-      __half2* h = reinterpret_cast<__half2*>(&o);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) h[k] = __floats2half2_rn(y[2 * k], y[2 * k + 1]);
-      *reinterpret_cast<uint4*>(p.D[prob] + static_cast<int64_t>(r) * p.C + c) = o;
-    }
-    __syncwarp();
-    cluster_sync();  // no CTA leaves while a peer still reads its partials
-  }
-
   // ---------------------------------------------------------------- teardown
+  __syncwarp();
   const bool aborted = *abort_flag != 0;
   if (warp == 0 && aborted && issued > 0 && lane == 0) {
     // loads in flight write this CTA's shared memory: allow them 100 us to
@@ -588,20 +587,17 @@ __global__ void __launch_bounds__(kTgThreads, 1)
     while (globaltimer() - t0 < 100000ull) __nanosleep(1000);
   }
   if (warp == 1 && crank == 0 && __any_sync(0xffffffffu, aborted)) {
-    tg_commit<CG>(drain);
+    tg_commit(drain);
     mbar_wait_drain(drain, 0);
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if constexpr (CG == 2) cluster_sync();  // the pair's MMAs, commits and arrivals are done
+  cluster_sync();  // the pair's MMAs, commits and arrivals are done
   if (warp == 1) {
     tc_fence_after();
-    if constexpr (CG == 2)
-      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(2 * kTgAccCols)
-                   : "memory");
-    else
-      tmem_dealloc(tmem_base, 2 * kTgAccCols);
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(2 * kTgAccCols)
+                 : "memory");
   }
 }
 

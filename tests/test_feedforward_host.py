@@ -85,15 +85,19 @@ def test_backward_refusals(lib, kw, status):
 
 def test_backward_workspace_size(lib):
     n = ctypes.c_size_t()
-    assert lib.aria_gated_bwd_workspace_size(4, 32, None) == 1
-    assert lib.aria_gated_bwd_workspace_size(0, 32, ctypes.byref(n)) == 1
-    assert lib.aria_gated_bwd_workspace_size(4, 2 ** 31, ctypes.byref(n)) == 1
-    # dG and dU, 256-byte aligned, then one row of partials
-    assert aq.gated_backward_workspace_size(1, 16) == 256 + 256 + 256
-    assert aq.gated_backward_workspace_size(4096, 6144) == 2 * (4096 * 6144 * 2) + 64 * 2 * 6144 * 4
-    for M in (1, 15, 16, 17, 1023, 1024, 1025, 1 << 20, (1 << 31) - 1):  # never more than 64 partials
-        parts = aq.gated_backward_workspace_size(M, 16) - 2 * ((M * 32 + 255) // 256 * 256)
-        assert 0 < parts <= 64 * 32 * 4 + 255
+    assert lib.aria_gated_bwd_workspace_size(4, 32, 64, None) == 1
+    assert lib.aria_gated_bwd_workspace_size(0, 32, 64, ctypes.byref(n)) == 1
+    assert lib.aria_gated_bwd_workspace_size(4, 2 ** 31, 64, ctypes.byref(n)) == 1
+    assert lib.aria_gated_bwd_workspace_size(4, 32, 0, ctypes.byref(n)) == 1
+    assert lib.aria_gated_bwd_workspace_size(2 ** 31 - 1, 2 ** 29, 64, ctypes.byref(n)) == 2
+    # dG and dU, 256-byte aligned, then one row of column partials
+    assert aq.gated_backward_workspace_size(1, 16, 16) == 256 + 256 + 256
+    up = lambda v: (v + 255) // 256 * 256
+    for M in (1, 15, 16, 17, 1023, 1024, 1025, 4096, 1 << 20):
+        for N, K in ((16, 16), (4096, 1024), (6144, 1536), (1024, 4096)):
+            extra = aq.gated_backward_workspace_size(M, N, K) - 2 * up(M * N * 2)
+            # at most 64 column partials, and up to 16 partials of dX
+            assert 0 < extra <= up(64 * 2 * N * 4) + up(16 * M * K * 4)
 
 
 def half(*s):

@@ -327,7 +327,7 @@ def test_backward_parts(want):
 def test_backward_workspace_needs_no_preparation():
     dH, X, Wg, Wu, G, U = bwd_inputs(200, 144, 208)
     ref = aq.gated_backward(dH, X, Wg, Wu, G, U)
-    n = aq.gated_backward_workspace_size(200, 144)
+    n = aq.gated_backward_workspace_size(200, 144, 208)
     ws = torch.full((n + 256,), 255, dtype=torch.uint8, device="cuda")  # every fp16 and fp32 a NaN
     for _ in range(2):
         got = aq.gated_backward(dH, X, Wg, Wu, G, U, workspace=ws[:n])
@@ -393,7 +393,7 @@ def test_training_step_captured_while_an_eager_one_lives(M):
     ins = [(normal(i, M, K), normal(i + 1, N, K, std=0.05), normal(i + 2, N, K, std=0.05), normal(i + 3, M, N)) for i in (1, 11)]
     new = lambda: ([torch.empty(M, N, dtype=torch.float16, device="cuda") for _ in range(2)],
                    tuple(torch.empty(*s, dtype=torch.float16, device="cuda") for s in ((M, K), (N, K), (N, K), (N,), (N,))),
-                   torch.empty(aq.gated_backward_workspace_size(M, N), dtype=torch.uint8, device="cuda"))
+                   torch.empty(aq.gated_backward_workspace_size(M, N, K), dtype=torch.uint8, device="cuda"))
     refs = []
     for t in ins:
         (G, U), out, ws = new()
