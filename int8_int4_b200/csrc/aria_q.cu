@@ -1045,7 +1045,7 @@ aria_status plan_tg(bool bmn, int bn, TgPlan* out) {
   p.off_out = p.off_b + static_cast<uint32_t>(ns) * p.b_stage;
   p.off_col = p.off_out + kTgStageBytes;
   p.off_bar = p.off_col + static_cast<uint32_t>(col_bytes);
-  out->smem = 1024 + p.off_bar + (2 * ns + 5) * 8 + 16;
+  out->smem = 1024 + p.off_bar + (2 * ns + 5 + kTgEpiWarps * kTgSlots) * 8 + 16;
   if (out->smem > static_cast<size_t>(di.smem_optin))
     return fail(ARIA_ERR_UNSUPPORTED, "shared memory plan too large");
   return ARIA_OK;
@@ -1136,8 +1136,9 @@ aria_status forward_tg(int kind, int64_t M, int64_t N, int64_t K, const void* X,
   p.steer = (steer && (alpha_dev || alpha != 0.0f)) ? steer : nullptr;
   p.alpha = p.steer ? alpha : 0.0f;
   p.alpha_dev = p.steer ? alpha_dev : nullptr;
-  p.res = static_cast<const __half*>(ea.res);
+  p.res = ea.res != nullptr;
   p.save = ea.G != nullptr;
+  if (ea.res && (s = out_map(&pl.m.R, ea.res, M, N)) != ARIA_OK) return s;
   if ((s = out_map(&pl.m.D[0], Y, M, N)) != ARIA_OK) return s;
   if (ea.G && ((s = out_map(&pl.m.D[1], ea.G, M, N)) != ARIA_OK || (s = out_map(&pl.m.D[2], ea.U, M, N)) != ARIA_OK))
     return s;

@@ -59,10 +59,14 @@ enum GemmKind : int { kQ8 = 1, kQ4 = 2, kW8A8 = 3, kS32 = 4, kF16 = 5 };
 //   kEpiPlain  y = main + bias + alpha v                    (aria_qgemm)
 //   kEpiAct    y = act(main + bias) + alpha v + R           (aria_qgemm_act)
 //   kEpiGated  h = act(main_g + bias_g) * (main_u + bias_u) (aria_qgemm_gated)
-// A gated tile holds 64 rows of the gate weight (TMEM lanes 0..63) and the 64
-// rows of the up weight for the same channels (lanes 64..127), so the
-// mainloop, the rings and the plans are those of a GEMM with 2 N rows; only
-// the epilogue brings the two halves of a channel together.
+// A gated tile holds 64 rows of the gate weight and the 64 rows of the up
+// weight for the same channels, so the mainloop, the rings and the plans are
+// those of a GEMM with 2 N rows; only the epilogue brings the two halves of a
+// channel together. Where the weights pass through registers on their way to
+// the MMA (q8, q4) each TMEM lane quarter gets 16 gate channels and the same
+// 16 channels of the up projection (gated_row), and a warp's epilogue trades
+// them by shuffles; elsewhere the gate has lanes 0..63 and the up projection
+// lanes 64..127, and pairs of warps trade through shared memory.
 enum EpiMode : int { kEpiPlain = 0, kEpiAct = 1, kEpiGated = 2 };
 
 constexpr int kTileN = 128;              // weight rows per tile (MMA M)
@@ -304,11 +308,11 @@ __device__ __forceinline__ float pre_act(uint32_t acc, float sx, const RowF& c) 
   return __fadd_rn(z, c.bias);
 }
 
-// act(z) + alpha v; a zero strength leaves the value's bits alone
+// act(z) + alpha v of two tokens; a zero strength leaves the value's bits alone
 template <int ACT>
-__device__ __forceinline__ float act_steer(float z, const RowF& c) {
-  const float y = act_fwd<ACT>(z);
-  return c.alpha != 0.0f ? __fmaf_rn(c.alpha, c.v, y) : y;
+__device__ __forceinline__ F2 act_steer2(F2 z, const RowF& c) {
+  const F2 y = act_fwd2<ACT>(z);
+  return c.alpha != 0.0f ? f2_fma(f2(c.alpha), f2(c.v), y) : y;
 }
 
 // W8A8 reference sequence: ((acc * s_x) * s_w) + bias + alpha*v in fp64, each
@@ -662,18 +666,16 @@ __device__ __forceinline__ void act_chunks(int c_first, int cs, int nchunk, uint
     tmem_ld_wait();
     if (c + cs >= nchunk) release();
     with_act(p.act, [&](auto tag) {
-      if (p.res) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float y = act_steer<decltype(tag)::value>(pre_act<KIND>(r[i], KIND == kW8A8 ? sxv[i] : 0.0f, rc), rc);
-          box[i * 32 + lane] = __float2half_rn(__fadd_rn(y, __half2float(box[i * 32 + lane])));
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float y = act_steer<decltype(tag)::value>(pre_act<KIND>(r[i], KIND == kW8A8 ? sxv[i] : 0.0f, rc), rc);
-          box[i * 32 + lane] = __float2half_rn(y);
-        }
+      for (int i = 0; i < 16; i += 2) {
+        F2 y = act_steer2<decltype(tag)::value>(f2(pre_act<KIND>(r[i], KIND == kW8A8 ? sxv[i] : 0.0f, rc),
+                                                   pre_act<KIND>(r[i + 1], KIND == kW8A8 ? sxv[i + 1] : 0.0f, rc)),
+                                                rc);
+        if (p.res)
+          y = f2_add(y, f2(__half2float(box[i * 32 + lane]), __half2float(box[(i + 1) * 32 + lane])));
+        const float2 o = f2_get(y);
+        box[i * 32 + lane] = __float2half_rn(o.x);
+        box[(i + 1) * 32 + lane] = __float2half_rn(o.y);
       }
     });
     epilogue_chunk_store<KIND>(c, nb, m0, lane, sbuf, p);
@@ -681,7 +683,7 @@ __device__ __forceinline__ void act_chunks(int c_first, int cs, int nchunk, uint
 }
 
 // ------------------------------------------------------- gated epilogue ---
-// The warps of one epilogue group (4 warps, one per TMEM lane quarter) work
+// W8A8, fp16: the warps of one epilogue group (4 warps, one per TMEM lane quarter) work
 // in pairs: warp q (0, 1) holds the gate's pre-activations of 32 channels,
 // warp q + 2 the up projection's of the same channels. They walk the same
 // chunks; for each, either warp hands over the half of the 16 tokens that
@@ -703,12 +705,81 @@ __device__ __forceinline__ bool pair_all(int warp, bool ok) {
   return r != 0;
 }
 
+// raw weight row (gate 0..63, up 64..127) of TMEM lane t, for q8 and q4
+template <int EPI>
+__device__ __forceinline__ int gated_row(int t) {
+  return EPI == kEpiGated ? ((t & 16) << 2) + ((t >> 5) << 4) + (t & 15) : t;
+}
+
 template <int ACT, int R>
 __device__ __forceinline__ void gated_out(const float (&own)[R], const float (&other)[R], bool up, __half (&h)[R]) {
 #pragma unroll
-  for (int j = 0; j < R; ++j) {
-    const float g = up ? other[j] : own[j], u = up ? own[j] : other[j];
-    h[j] = __float2half_rn(act_fwd<ACT>(g) * u);
+  for (int j = 0; j < R; j += 2) {
+    const F2 o = f2(own[j], own[j + 1]), x = f2(other[j], other[j + 1]);
+    const F2 g = up ? x : o, u = up ? o : x;
+    const float2 y = f2_get(f2_mul(act_fwd2<ACT>(g), u));
+    h[j] = __float2half_rn(y.x);
+    h[j + 1] = __float2half_rn(y.y);
+  }
+}
+
+// q8, q4: the warp holds 16 gate channels in its lanes 0..15 and the same
+// channels of the up projection in lanes 16..31. Of a chunk's 16 tokens the
+// gate lanes finish 0..7 and the up lanes 8..15: each hands the other half
+// over by shuffle, and the results leave through a [16 tokens][16 channels]
+// box as 16-byte stores.
+template <int KIND, class Release>
+__device__ __forceinline__ void gated_chunks_dq(int c_first, int cs, int nchunk, uint32_t tacc, int lane,
+                                                uint8_t* sb0, const RowF& rc, int nb, int m0,
+                                                const GemmParams& p, Release release) {
+  if (c_first >= nchunk) {
+    release();
+    return;
+  }
+  const bool up = lane >= 16;
+  const int ch = lane & 15;
+  __half* box = reinterpret_cast<__half*>(sb0);
+  const int srow = lane >> 1, scol = (lane & 1) * 8;  // this lane's 16 bytes of a box
+  const bool n_in = nb + scol < p.N;
+  uint32_t r[16];
+  tmem_ld16(tacc + c_first * 16, r);
+  for (int c = c_first; c < nchunk; c += cs) {
+    tmem_ld_wait();
+    float z[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) z[i] = pre_act<KIND>(r[i], 0.0f, rc);
+    // the next chunk's accumulators travel while this one is computed
+    if (c + cs < nchunk) tmem_ld16(tacc + (c + cs) * 16, r);
+    else release();
+    float own[8], other[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      own[j] = up ? z[8 + j] : z[j];
+      other[j] = __shfl_xor_sync(0xffffffffu, up ? z[j] : z[8 + j], 16);
+    }
+    const int m = m0 + c * 16 + srow;
+    const int64_t o = static_cast<int64_t>(m) * p.N + nb + scol;
+    const bool in = m < p.M && n_in;
+    if (p.G) {  // a training step keeps the pre-activations: a box of either
+      __half* zb = box + 256 + (up ? 256 : 0);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) zb[i * 16 + ch] = __float2half_rn(z[i]);
+    }
+    __half h[8];
+    with_act(p.act, [&](auto tag) { gated_out<decltype(tag)::value, 8>(own, other, up, h); });
+#pragma unroll
+    for (int j = 0; j < 8; ++j) box[((up ? 8 : 0) + j) * 16 + ch] = h[j];
+    __syncwarp();
+    const uint4 v = reinterpret_cast<const uint4*>(box)[lane];
+    if (in) *reinterpret_cast<uint4*>(reinterpret_cast<__half*>(p.Y) + o) = v;
+    if (p.G) {
+      const uint4 vg = reinterpret_cast<const uint4*>(box + 256)[lane], vu = reinterpret_cast<const uint4*>(box + 512)[lane];
+      if (in) {
+        *reinterpret_cast<uint4*>(p.G + o) = vg;
+        *reinterpret_cast<uint4*>(p.U + o) = vu;
+      }
+    }
+    __syncwarp();  // the boxes have been read before the next chunk writes them
   }
 }
 
@@ -788,8 +859,8 @@ __device__ __forceinline__ void gated_chunks(int c_first, int cs, int nchunk, ui
 }
 
 // Split-K: sum of the cluster's partials and the gated epilogue for token rows
-// [mb, me) of the tile. red[token][128] holds the gate's 64 channels, then
-// the up projection's. Lanes 0..15 of a warp take one token row, lanes
+// [mb, me) of the tile. red[token][128] is in the order of the TMEM lanes (see
+// EpiMode). Lanes 0..15 of a warp take one token row, lanes
 // 16..31 the next, four channels each; partials are added in rank order.
 template <int KIND>
 __device__ __forceinline__ void split_gated(const uint8_t* red, int n0, int m0, int mb, int me, int warp,
@@ -803,6 +874,9 @@ __device__ __forceinline__ void split_gated(const uint8_t* red, int n0, int m0, 
     rg[j] = row_f(row_raw<KIND, kEpiGated>(n + j, p, false), 0.0f);
     ru[j] = row_f(row_raw<KIND, kEpiGated>(n + j, p, true), 0.0f);
   }
+  constexpr bool kDq = KindTraits<KIND>::kDequant;
+  const int lg = kDq ? (nl >> 4) * 32 + (nl & 15) : nl;  // the gate's words of a row
+  constexpr uint32_t kUp = kDq ? 64u : 256u;             // bytes from there to the up projection's
   const uint32_t red_u32 = smem_u32(red);
   for (int ml0 = mb + 2 * warp; ml0 < me; ml0 += 2 * kWarps) {
     const int ml = ml0 + (lane >> 4);
@@ -813,9 +887,9 @@ __device__ __forceinline__ void split_gated(const uint8_t* red, int n0, int m0, 
 #pragma unroll
     for (int q = 0; q < kMaxSplits; ++q) {
       if (q < p.splits) {
-        const uint32_t a = mapa_shared(red_u32 + static_cast<uint32_t>((ml * 128 + nl) * 4), q);
+        const uint32_t a = mapa_shared(red_u32 + static_cast<uint32_t>((ml * 128 + lg) * 4), q);
         vg[q] = ld_dsmem_v4(a);
-        vu[q] = ld_dsmem_v4(a + 256u);
+        vu[q] = ld_dsmem_v4(a + kUp);
       }
     }
     uint4 g = vg[0], u = vu[0];
@@ -1123,6 +1197,7 @@ __global__ void __launch_bounds__(KindTraits<KIND>::kThreads, 1)
     uint32_t rph = 0, aph = 0;
     bool ok = true;
     WaitClock wc_raw, wc_empty;  // trace builds: time waiting for weights / for a free stage
+    const int tr = gated_row<EPI>(t);  // the raw row that becomes row t of A
     for (int tile = tile0; tile < p.tiles && ok; tile += tstep) {
       for (int i = 0; i < nu && ok; ++i) {
         wc_raw.start();
@@ -1136,10 +1211,10 @@ __global__ void __launch_bounds__(KindTraits<KIND>::kThreads, 1)
         for (int c = 0; c < 8; ++c) {  // the 16-byte chunks of this group's K blocks
           v[c] = make_uint4(0u, 0u, 0u, 0u);
           if (ngrp == 1 || (c / (8 / T::kKbPerUnit)) % 2 == grp)
-            v[c] = *reinterpret_cast<const uint4*>(src + sw128(t, c));
+            v[c] = *reinterpret_cast<const uint4*>(src + sw128(tr, c));
         }
         uint4 sc = make_uint4(0, 0, 0, 0);
-        if constexpr (KIND == kQ4) sc = *reinterpret_cast<const uint4*>(src + kATile + t * 16);
+        if constexpr (KIND == kQ4) sc = *reinterpret_cast<const uint4*>(src + kATile + tr * 16);
         // The slot's next writer is a TMA load (async proxy): order this
         // thread's generic-proxy reads of it before that write. Without
         // the proxy fence the release of the arrive alone let a refill land
@@ -1239,6 +1314,12 @@ __global__ void __launch_bounds__(KindTraits<KIND>::kThreads, 1)
     return ok;
   };
 
+  // the channel of the tile, and the projection, that TMEM lane t holds
+  auto lane_chan = [](int t) {
+    return EPI != kEpiGated ? t : T::kDequant ? ((t >> 5) << 4) + (t & 15) : (t & 63);
+  };
+  auto lane_up = [](int t) { return EPI == kEpiGated && (T::kDequant ? (t & 16) != 0 : t >= 64); };
+
   // The CTA's last tile, for a warp that helps with it: the constants of the
   // channel in its row t of the tile (loaded before the wait for the
   // accumulator), and its chunks c0, c0 + cs, ...
@@ -1248,7 +1329,7 @@ __global__ void __launch_bounds__(KindTraits<KIND>::kThreads, 1)
     else if constexpr (EPI == kEpiAct)
       return row_f(row_raw<KIND>(n0 + t, p), p.steer ? steer_alpha(p) : 0.0f);
     else
-      return row_f(row_raw<KIND, EPI>(n0 + (t & 63), p, t >= 64), 0.0f);
+      return row_f(row_raw<KIND, EPI>(n0 + lane_chan(t), p, lane_up(t)), 0.0f);
   };
   auto tail_chunks = [&](int c0, int cs, uint32_t tacc, uint8_t* sb0, const auto& rc, int n0, int m0,
                          const float* sx_tile) {
@@ -1258,6 +1339,8 @@ __global__ void __launch_bounds__(KindTraits<KIND>::kThreads, 1)
                             [] {});
     else if constexpr (EPI == kEpiAct)
       act_chunks<KIND>(c0, cs, p.BN / 16, tacc, lane, sb0, rc, sx_tile, n0 + (warp & 3) * 32, m0, p, [] {});
+    else if constexpr (T::kDequant)
+      gated_chunks_dq<KIND>(c0, cs, p.BN / 16, tacc, lane, sb0, rc, n0 + (warp & 3) * 16, m0, p, [] {});
     else
       gated_chunks<KIND>(c0, cs, p.BN / 16, tacc, warp, lane, sb0, rc, sx_tile, n0 + (warp & 1) * 32, m0, p,
                          [] {});
@@ -1404,18 +1487,15 @@ __global__ void __launch_bounds__(KindTraits<KIND>::kThreads, 1)
       const bool ok = dequant_rows(t, 0, (KIND == kQ4 && p.tmem_a) ? 2 : 1);
       // The CTA's last tile: these warps take its odd epilogue chunks, with
       // store boxes staged in the now idle raw-weight ring.
-      // (gated: its warps work in pairs, so one that gave up stays with its
-      // partner until they have agreed to skip the tile)
-      if ((ok || EPI == kEpiGated) && !split && tile0 < p.tiles) {
+      if (ok && !split && tile0 < p.tiles) {
         const int ti = (p.tiles - tile0 + tstep - 1) / tstep - 1;
         const int tile = tile0 + ti * tstep;
         const int b = ti & 1;
         const int n0 = (tile % p.tiles_n) * kChans;
         const int m0 = (tile / p.tiles_n) * p.BN;
         const auto rc = tail_consts(t, n0);
-        bool ok2 = ok && mbar_wait(acc_last, 0, abort_flag, 10, wlim);
+        bool ok2 = mbar_wait(acc_last, 0, abort_flag, 10, wlim);
         ok2 = __all_sync(0xffffffffu, ok2);
-        if constexpr (EPI == kEpiGated) ok2 = pair_all(warp, ok2);
         if (ok2) {
           tc_fence_after();
           const uint32_t tacc = tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16) + b * kAccCols;
@@ -1442,8 +1522,8 @@ __global__ void __launch_bounds__(KindTraits<KIND>::kThreads, 1)
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     if (!split) {
       uint8_t* sbuf0 = stage + e * kWarpStage;
-      const int tc = EPI == kEpiGated ? (t & 63) : t;  // channel within the tile
-      const bool up = EPI == kEpiGated && t >= 64;
+      const int tc = lane_chan(t);  // channel within the tile
+      const bool up = lane_up(t);
       const float alpha = p.steer ? steer_alpha(p) : 0.0f;
       // The channel constants and (W8A8) token scales of a tile are loaded
       // one tile ahead, so their latency hides behind the previous tile's
@@ -1480,7 +1560,7 @@ __global__ void __launch_bounds__(KindTraits<KIND>::kThreads, 1)
         if constexpr (KIND == kW8A8) named_bar(1, nep);
         bool ok = mbar_wait(acc_full + b, (ti >> 1) & 1, abort_flag, 8, wlim);
         ok = __all_sync(0xffffffffu, ok);  // warp-uniform before .sync.aligned TMEM loads
-        if constexpr (EPI == kEpiGated) ok = pair_all(warp, ok);
+        if constexpr (EPI == kEpiGated && !T::kDequant) ok = pair_all(warp, ok);
         if (ok) {
           if (te == 0 && ti == 0) ARIA_STAMP(6);
           tc_fence_after();
@@ -1502,6 +1582,8 @@ __global__ void __launch_bounds__(KindTraits<KIND>::kThreads, 1)
           else if constexpr (EPI == kEpiAct)
             act_chunks<KIND>(cgrp, cs, p.BN / 16, tacc, lane, sbuf0, rf, sxc, n0 + (warp & 3) * 32, m0, p,
                              release);
+          else if constexpr (T::kDequant)
+            gated_chunks_dq<KIND>(cgrp, cs, p.BN / 16, tacc, lane, sbuf0, rf, n0 + (warp & 3) * 16, m0, p, release);
           else
             gated_chunks<KIND>(cgrp, cs, p.BN / 16, tacc, warp, lane, sbuf0, rf, sxc, n0 + (warp & 1) * 32, m0,
                                p, release);
@@ -1535,7 +1617,7 @@ __global__ void __launch_bounds__(KindTraits<KIND>::kThreads, 1)
         for (int j = threadIdx.x; j < p.BN; j += 128) hsx[j] = (m0 + j < p.M) ? ld_dep_f32(p.sx + m0 + j) : 0.0f;
       named_bar(2, 128);
     }
-    if constexpr (EPI == kEpiGated) ok = pair_all(warp, ok);
+    if constexpr (EPI == kEpiGated && !T::kDequant) ok = pair_all(warp, ok);
     if (ok) {
       tc_fence_after();
       tail_chunks(2, 3, tmem_base + (static_cast<uint32_t>(warp * 32) << 16) + (ti & 1) * kAccCols,
@@ -1647,7 +1729,8 @@ __global__ void __launch_bounds__(KindTraits<KIND>::kThreads, 1)
               with_act(p.act, [&](auto tag) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                  const float y = act_steer<decltype(tag)::value>(pre_act<KIND>(a4[k], sxm, rf[k]), rf[k]);
+                  const float z = pre_act<KIND>(a4[k], sxm, rf[k]);
+                  const float y = f2_get(act_steer2<decltype(tag)::value>(f2(z), rf[k])).x;
                   h[k] = __float2half_rn(p.res ? __fadd_rn(y, __half2float(hr[k])) : y);
                 }
               });

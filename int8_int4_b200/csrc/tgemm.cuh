@@ -53,19 +53,21 @@ namespace aria {
 
 enum TgMode : int { kTgGrad = 0, kTgAct = 1, kTgGated = 2 };
 
-constexpr int kTgThreads = 384;
 constexpr int kTgEpiWarps = 8;
+constexpr int kTgThreads = 128 + 32 * kTgEpiWarps;
+constexpr int kTgEpiStep = kTgEpiWarps / 4;  // warps per TMEM lane quarter: they share a tile's column units
 constexpr int kTgRows = 128;              // rows per CTA; a pair's tile has twice as many
 constexpr uint32_t kTgATile = 16384;      // 128 rows x 64 fp16 (or 128 int8) of k
 constexpr uint32_t kTgAccCols = 256;
 constexpr uint32_t kTgBox = 32 * 64;      // output box of a warp: 32 rows x 32 fp16
-constexpr int kTgSlots = 2;               // store boxes per epilogue warp (both together: 32 x 32 fp32)
+constexpr int kTgSlots = 3;               // boxes per epilogue warp (two together hold 32 x 32 fp32)
 constexpr uint32_t kTgStageBytes = kTgEpiWarps * kTgSlots * kTgBox;
 
 struct TgMaps {
   CUtensorMap A[4];  // forward: X; gradients: dG, dU as rows of tokens, then as rows of channels
   CUtensorMap B[3];  // forward: W (gated: gate, up); gradients: Wg, Wu, X
   CUtensorMap D[3];  // forward: Y or H, G, U; gradients: dX (split k: its fp32 partials), dWg, dWu
+  CUtensorMap R;     // kTgAct: the residual
 };
 
 // Column sums left over from an earlier kernel of the call: P rows of fp32
@@ -108,7 +110,7 @@ struct TgParams {
   const float* steer;      // kTgAct
   float alpha;
   const float* alpha_dev;
-  const __half* res;       // kTgAct: [R,C] or null; may be Y itself
+  int res;                 // kTgAct: add the residual (may be Y itself)
   int save;                // kTgGated: keep the pre-activations
   ColSum colsum;
 };
@@ -166,6 +168,15 @@ __device__ __forceinline__ void tg_load(const CUtensorMap* m, uint32_t bar, void
       "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
+
+// a load that reports to a barrier of this CTA
+__device__ __forceinline__ void tg_load_local(const CUtensorMap* m, uint64_t* bar, void* dst, int32_t x, int32_t y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(x), "r"(y)
       : "memory");
 }
 
@@ -246,7 +257,8 @@ __global__ void __launch_bounds__(kTgThreads, 1)
   uint64_t* acc_full = empty + p.nstage;   // [2]
   uint64_t* acc_empty = acc_full + 2;      // [2], the pair's first CTA's
   uint64_t* drain = acc_empty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* res_full = drain + 1;          // kTgAct: [kTgEpiWarps][kTgSlots]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(res_full + kTgEpiWarps * kTgSlots);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   if (threadIdx.x == 0) {
@@ -259,6 +271,7 @@ __global__ void __launch_bounds__(kTgThreads, 1)
       mbar_init(acc_empty + i, 2 * kTgEpiWarps);
     }
     mbar_init(drain, 1);
+    for (int i = 0; i < kTgEpiWarps * kTgSlots; ++i) mbar_init(res_full + i, 1);
     *abort_flag = 0;
     fence_mbar_init();
     if constexpr (MODE != kTgGrad) {  // (a gradient launch fills only the maps that it uses)
@@ -436,7 +449,7 @@ __global__ void __launch_bounds__(kTgThreads, 1)
     // ----------------------------------------------------------- epilogue
     const int e = warp - 4, te = threadIdx.x - 128;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const int cg = e >> 2;  // this warp takes 32-column units cg, cg + 2, ...
+    const int cg = e >> 2;  // this warp takes 32-column units cg, cg + kTgEpiStep, ...
     const uint32_t release0 = mapa_shared(smem_u32(acc_empty), 0);
     const float alpha = (MODE == kTgAct && p.steer) ? (p.alpha_dev ? *p.alpha_dev : p.alpha) : 0.0f;
     // column constants of an item, one item ahead: bias, scale, steering
@@ -457,7 +470,38 @@ __global__ void __launch_bounds__(kTgThreads, 1)
     TgItem it, nx;
     bool valid = item_at(0, nx);
     if constexpr (MODE != kTgGrad) col_load(valid, nx, cv);
-    int nst = 0;
+    int slot = 0;       // the next unit's box
+    uint32_t rph = 0;   // parity of its residual's arrival
+    // kTgAct: the residual of a unit is loaded by TMA into the box that will
+    // carry the unit's result, kTgSlots - 1 units ahead and across items (the
+    // lane reads its row of the box, adds, and writes the sum in its place).
+    // Read directly, 16 bytes per row and lane, it bounded the epilogue: 53-61
+    // us at M = 4096, N = 6144, K = 1536, W8A8.
+    TgItem pit;
+    int pi = 0, pc = cg, pslot = 0;
+    bool pvalid = valid;
+    pit = nx;
+    auto res_issue = [&] {  // lane 0 issues the load of the next unit in line
+      if (!pvalid) return;
+      if (lane == 0) {
+        bulk_wait_read<1>();  // all but the newest store have read their boxes
+        uint64_t* bar = res_full + e * kTgSlots + pslot;
+        mbar_arrive_expect_tx(bar, kTgBox);
+        tg_load_local(&tm.R, bar, boxes + pslot * kTgBox, pit.c0 + pc * 32, pit.r0 + (warp & 3) * 32);
+      }
+      if (++pslot == kTgSlots) pslot = 0;
+      pc += kTgEpiStep;
+      if (pc * 32 >= chans || pit.c0 + pc * 32 >= p.C) {
+        pc = cg;
+        do {  // (a narrow last column tile may hold no unit of this warp)
+          pvalid = item_at(++pi, pit);
+        } while (pvalid && pit.c0 + pc * 32 >= p.C);
+      }
+    };
+    if (MODE == kTgAct && p.res) {
+      while (pvalid && pit.c0 + pc * 32 >= p.C) pvalid = item_at(++pi, pit);
+      for (int k = 0; k < kTgSlots - 1; ++k) res_issue();
+    }
     for (int i = 0; valid; ++i) {
       it = nx;
       valid = item_at(i + 1, nx);
@@ -465,7 +509,8 @@ __global__ void __launch_bounds__(kTgThreads, 1)
       float* cb = col + b * 3 * kTgAccCols;
       if constexpr (MODE != kTgGrad) {
 #pragma unroll
-        for (int k = 0; k < 3; ++k) cb[k * kTgAccCols + te] = cv[k];
+        for (int k = 0; k < 3; ++k)
+          if (te < static_cast<int>(kTgAccCols)) cb[k * kTgAccCols + te] = cv[k];
         named_bar(1, kTgEpiWarps * 32);  // and every reader of this buffer two items ago is done
         col_load(valid, nx, cv);
       }
@@ -473,7 +518,6 @@ __global__ void __launch_bounds__(kTgThreads, 1)
       const int rows = MODE == kTgGrad ? (it.type == 0 ? p.M : p.N) : p.R;
       const int cols = MODE == kTgGrad ? p.K : p.C;
       const bool row_in = r < rows;
-      const int64_t ro = static_cast<int64_t>(r) * cols;
       float sx = 1.0f;
       if constexpr (I8) sx = row_in ? ld_dep_f32(p.sx + r) : 0.0f;
       bool ok = mbar_wait(acc_full + b, (i >> 1) & 1, abort_flag, 43);
@@ -481,13 +525,19 @@ __global__ void __launch_bounds__(kTgThreads, 1)
       if (!ok) continue;  // (stays with the named barriers of later items)
       tc_fence_after();
       const uint32_t tacc = tmem_base + lane_off + b * kTgAccCols;
-      // units of 32 columns; a result goes through a store box of the warp's
-      // own and leaves by TMA, which clips the box at the tensor's edges
-      auto box_store = [&](const CUtensorMap* m, const F2 (&y)[16], int c0) {
-        uint8_t* box = boxes + (nst & (kTgSlots - 1)) * kTgBox;
-        ++nst;
-        if (lane == 0) bulk_wait_read<kTgSlots - 1>();  // the box's last store has read it
+      // units of 32 columns; a result goes through one of the warp's boxes and
+      // leaves by TMA, which clips the box at the tensor's edges
+      if constexpr (MODE == kTgGrad) {  // the fp32 box of a share of k covers two others
+        if (lane == 0) bulk_wait_read<0>();
         __syncwarp();
+      }
+      auto box_store = [&](const CUtensorMap* m, const F2 (&y)[16], int c0) {
+        uint8_t* box = boxes + slot * kTgBox;
+        if (++slot == kTgSlots) slot = 0;
+        if (MODE != kTgAct || !p.res) {  // (with a residual the box is the warp's since its load was issued)
+          if (lane == 0) bulk_wait_read<kTgSlots - 1>();  // the box's last store has read it
+          __syncwarp();
+        }
         tg_box_row(box, lane, y);
         fence_proxy_async_smem();
         __syncwarp();
@@ -497,7 +547,7 @@ __global__ void __launch_bounds__(kTgThreads, 1)
         }
       };
       const int nunit32 = (chans + 31) / 32;
-      for (int c = cg; c < nunit32; c += 2) {
+      for (int c = cg; c < nunit32; c += kTgEpiStep) {
         const int c0 = it.c0 + c * 32;
         if (c0 >= cols) break;
         uint32_t v[32];
@@ -522,12 +572,6 @@ __global__ void __launch_bounds__(kTgThreads, 1)
             box_store(&tm.D[it.type == 0 ? 0 : 1 + it.src], z, c0);
           }
         } else if constexpr (MODE == kTgAct) {
-          uint4 rv[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            rv[j] = make_uint4(0u, 0u, 0u, 0u);
-            if (p.res && row_in && c0 + 8 * j < p.C) rv[j] = ld_dep_v4(p.res + ro + c0 + 8 * j);  // C % 16 == 0
-          }
           tmem_ld_wait();
           tg_pre<I8>(v, sx, cb + kTgAccCols + c * 32, cb + c * 32, z);
           with_act(p.act, [&](auto tag) {
@@ -543,14 +587,23 @@ __global__ void __launch_bounds__(kTgThreads, 1)
             }
           }
           if (p.res) {
-            const __half2* hr = reinterpret_cast<const __half2*>(rv);
+            mbar_wait(res_full + e * kTgSlots + slot, rph, abort_flag, 45);
+            if (slot == kTgSlots - 1) rph ^= 1u;
+            __syncwarp();
+            const uint8_t* box = boxes + slot * kTgBox;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const float2 f = __half22float2(hr[j]);
-              z[j] = f2_add(z[j], f2(f.x, f.y));
+            for (int j = 0; j < 4; ++j) {
+              const uint4 rv = *reinterpret_cast<const uint4*>(box + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4));
+              const __half2* hr = reinterpret_cast<const __half2*>(&rv);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float2 f = __half22float2(hr[k]);
+                z[4 * j + k] = f2_add(z[4 * j + k], f2(f.x, f.y));
+              }
             }
           }
           box_store(&tm.D[0], z, c0);
+          if (p.res) res_issue();
         } else {
           uint32_t w[32];
           tmem_ld32(tacc + chans + c * 32, w);
