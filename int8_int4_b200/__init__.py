@@ -592,7 +592,11 @@ def gated_backward(dH: torch.Tensor, X, Wg, Wu, G: torch.Tensor, U: torch.Tensor
     raw = _here(dev, stream)
     with contextlib.nullcontext(raw) if raw is not None else _running_on(dev, stream) as raw:
         if out is None:
-            out = tuple([torch.empty(sh, dtype=f16, device=dev) if on else None for on, sh in zip(asked, shapes)])
+            dX = torch.empty_like(X) if input_grad and X is not None else (
+                torch.empty(M, K, dtype=f16, device=dev) if input_grad else None)
+            dWg, dWu = torch.empty((2, N, K), dtype=f16, device=dev).unbind() if weight_grad else (None, None)
+            dbg, dbu = torch.empty((2, N), dtype=f16, device=dev).unbind() if bias_grad else (None, None)
+            out = (dX, dWg, dWu, dbg, dbu)
         ws = workspace if workspace is not None else torch.empty(need, dtype=torch.uint8, device=dev)
         _check(lib.aria_gated_bwd(a, M, N, K, *pin, *[None if t is None else t.data_ptr() for t in out],
                                   ws.data_ptr(), ws.numel(), raw))

@@ -1100,22 +1100,68 @@ aria_status out_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols
   return make_map(m, base, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, rows, cols, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
-// The forward operators over many tokens (fp16, W8A8) on the token-major kernel.
-// Measured at N = 6144, K = 1536, M = 4096 against the channel-major kernel:
-// gated fp16 with G and U kept 121 against 203 us, gated W8A8 62 against 97.
-bool use_tg(int kind, int64_t M) {
-  return (kind == aria::kF16 || kind == aria::kW8A8) && M > 512;
+// The forward operators on the token-major kernel (fp16, W8A8): the tile
+// width, and whether it is expected to be faster than the channel-major one.
+//
+// Times in us, a model of the two kernels: a K block of a pair takes
+// max(2 BN, 256 + BN) cycles (the tensor core's and the shared memory's), one
+// of the channel-major kernel 2 (128 + BN); a tile's epilogue overlaps the
+// next tile's mainloop in part, and the last one stands alone. The five
+// remaining constants are fitted to a sweep over five weight shapes and nine
+// token counts from 48 to 4096, where the choice for the gated operator then
+// costs 0.6 % over the best of the four variants on average.
+struct TgChoice {
+  int bn = 256;
+  double us = 0.0;
+};
+
+TgChoice choose_tg(bool gated, int64_t M, int64_t N, int64_t nkb) {
+  TgChoice best;
+  const int64_t pairs = dev_info().sms / 2, tr = (M + 2 * aria::kTgRows - 1) / (2 * aria::kTgRows);
+  for (int bn : {256, 192, 128}) {
+    const int chans = gated ? bn / 2 : bn;
+    const int64_t waves = (tr * ((N + chans - 1) / chans) + pairs - 1) / pairs;
+    const double kb = std::max(2 * bn, 256 + bn) / 1850.0;  // us per K block
+    const double epi = bn / 64 * (gated ? 0.45 : 1.5);      // a tile's epilogue
+    const double main = static_cast<double>(nkb) * kb;
+    const double t = 2.8 + epi + static_cast<double>(waves) * (1.5 + std::max(main, epi) + 0.75 * std::min(main, epi));
+    if (best.us == 0.0 || t < best.us) best = TgChoice{bn, t};
+  }
+  return best;
+}
+
+// Measured: gated fp16 over N = 6144, K = 1536 takes 12.8 us against 21.1 at
+// M = 203 and 110 against 163 at M = 4096, but over N = 1536, K = 6144 (few
+// tiles, which only the channel-major kernel splits along K) 28 against 24 at
+// M = 432; a linear with residual wins only where its products outweigh the
+// epilogue: W8A8 at M = 4096, N = 1536, K = 6144 33 against 39 us, at K = 1536
+// 18.4 against 17.6.
+bool use_tg(int kind, bool gated, int64_t M, int64_t N, int64_t K, int* bn) {
+  using namespace aria;
+  if ((kind != kF16 && kind != kW8A8) || M < 128) return false;
+  const int64_t nkb = (K * (kind == kF16 ? 2 : 1) + 127) / 128;
+  const TgChoice tg = choose_tg(gated, M, N, nkb);
+  *bn = tg.bn;
+  if (!gated) return 2.0 * static_cast<double>(M) * N * K >= 3e10;
+  Plan pl;
+  if (plan_gemm(kind, kEpiGated, M, N, K, &pl) != ARIA_OK) return false;
+  const int64_t sms = dev_info().sms, ctas = static_cast<int64_t>(pl.p.tiles) * pl.p.splits;
+  const double kb = 2.0 * (128 + pl.p.BN) / 1850.0, epi = pl.p.BN * 0.022;
+  const double main = static_cast<double>(nkb) / pl.p.splits * kb;
+  const double chan = 0.5 + (pl.p.splits > 1 ? 6.0 : epi) +
+                      static_cast<double>((ctas + sms - 1) / sms) * (std::max(main, epi) + 0.8 * std::min(main, epi));
+  return tg.us < chan;
 }
 
 template <int MODE>
-aria_status forward_tg(int kind, int64_t M, int64_t N, int64_t K, const void* X, const float* sx, const void* W,
+aria_status forward_tg(int kind, int bn, int64_t M, int64_t N, int64_t K, const void* X, const float* sx, const void* W,
                        const void* scales, const void* bias, const float* steer, float alpha,
                        const float* alpha_dev, void* Y, const EpiArgs& ea, cudaStream_t st) {
   using namespace aria;
   const bool i8 = kind == kW8A8;
   TgPlan pl;
   const int kelems = i8 ? 128 : 64;
-  aria_status s = plan_tg(false, 256, &pl);
+  aria_status s = plan_tg(false, bn, &pl);
   if (s != ARIA_OK) return s;
   TgParams& p = pl.p;
   const int chans = MODE == kTgGated ? p.BN / 2 : p.BN;
@@ -1187,7 +1233,7 @@ struct BwdPlan {
   aria::TgSched sched{};
 };
 
-BwdPlan bwd_plan(int64_t M, int64_t N, int64_t K, bool dx, bool dw) {
+BwdPlan make_bwd_plan(int64_t M, int64_t N, int64_t K, bool dx, bool dw, int units) {
   using namespace aria;
   BwdPlan pl;
   // at most 64 partials per column (their sum is read once more), and at
@@ -1197,7 +1243,6 @@ BwdPlan bwd_plan(int64_t M, int64_t N, int64_t K, bool dx, bool dw) {
   auto tiles = [](int64_t rows, int64_t cols) {
     return (rows + 2 * kTgRows - 1) / (2 * kTgRows) * ((cols + kBwdBn - 1) / kBwdBn);
   };
-  const int units = dev_info().sms / 2;
   const int64_t tx = dx ? tiles(M, K) : 0, lx = 2 * ((N + 63) / 64);
   const int64_t tw = dw ? 2 * tiles(N, K) : 0, lw = (M + 63) / 64;
   // Shares of k for dX: each more than one costs a further launch that reads
@@ -1228,6 +1273,22 @@ BwdPlan bwd_plan(int64_t M, int64_t N, int64_t K, bool dx, bool dw) {
   }
   pl.units = static_cast<int>(std::min<int64_t>(units, std::max<int64_t>(1, tx * pl.parts + tw)));
   return pl;
+}
+
+// The plan of the sizes asked for last (it takes a few us to make, and a
+// training loop asks for the same one three times a call).
+BwdPlan bwd_plan(int64_t M, int64_t N, int64_t K, bool dx, bool dw) {
+  struct Entry {
+    int64_t M = 0, N = 0, K = 0;
+    int units = 0;
+    BwdPlan pl;
+  };
+  static thread_local Entry last[4];
+  const int units = dev_info().sms / 2;
+  Entry& e = last[(dx ? 1 : 0) + (dw ? 2 : 0)];
+  if (e.M != M || e.N != N || e.K != K || e.units != units)
+    e = Entry{M, N, K, units, make_bwd_plan(M, N, K, dx, dw, units)};
+  return e.pl;
 }
 
 // keeps every byte count below 2^48 (no device holds such tensors)
@@ -1280,8 +1341,9 @@ ARIA_API aria_status aria_qgemm_act(aria_format fmt, int group, int64_t M, int64
   EpiArgs ea;
   ea.act = act;
   ea.res = residual;
-  if (use_tg(kind, M))
-    return forward_tg<aria::kTgAct>(kind, M, N, K, X, sx, Wq, scales, bias, steer_vec, alpha, alpha_dev, Y, ea, st);
+  int bn = 0;
+  if (use_tg(kind, false, M, N, K, &bn))
+    return forward_tg<aria::kTgAct>(kind, bn, M, N, K, X, sx, Wq, scales, bias, steer_vec, alpha, alpha_dev, Y, ea, st);
   return qgemm_impl<aria::kEpiAct>(kind, M, N, K, X, sx, Wq, scales, bias, steer_vec, alpha, alpha_dev, Y, st,
                                    ea);
 }
@@ -1311,8 +1373,9 @@ ARIA_API aria_status aria_qgemm_gated(aria_format fmt, int group, int64_t M, int
   ea.bias_u = bias_u;
   ea.G = G;
   ea.U = U;
-  if (use_tg(kind, M))
-    return forward_tg<aria::kTgGated>(kind, M, N, K, X, sx, Wg, scales_g, bias_g, nullptr, 0.0f, nullptr, H, ea,
+  int bn = 0;
+  if (use_tg(kind, true, M, N, K, &bn))
+    return forward_tg<aria::kTgGated>(kind, bn, M, N, K, X, sx, Wg, scales_g, bias_g, nullptr, 0.0f, nullptr, H, ea,
                                       static_cast<cudaStream_t>(stream));
   return qgemm_impl<aria::kEpiGated>(kind, M, N, K, X, sx, Wg, scales_g, bias_g, nullptr, 0.0f, nullptr, H,
                                      static_cast<cudaStream_t>(stream), ea);

@@ -27,7 +27,7 @@ namespace aria {
 constexpr int kGbThreads = 256;
 constexpr int kGbCols = 128;
 
-__global__ void __launch_bounds__(kGbThreads)
+__global__ void __launch_bounds__(kGbThreads, 4)
     gated_bwd_kernel(const __half* __restrict__ dH, const __half* __restrict__ G, const __half* __restrict__ U,
                      __half* __restrict__ dG, __half* __restrict__ dU, float* __restrict__ part, int M, int N,
                      int rows, int act) {
@@ -42,46 +42,49 @@ __global__ void __launch_bounds__(kGbThreads)
   for (int i = 0; i < 4; ++i) sg[i] = su[i] = f2(0.0f);
   if (c < N) {  // N % 16 == 0: 8 columns are wholly in or out
     with_act(act, [&](auto tag) {
-      constexpr int kUnroll = 2;
-      for (int r = rb + ty; r < re; r += 16 * kUnroll) {
-        uint4 vh[kUnroll], vg[kUnroll], vu[kUnroll];
+      // two rows' loads are always in flight: the next row's and the one's
+      // behind it
+      uint4 v[2][3];
+      auto load = [&](int r, uint4 (&w)[3]) {
+        if (r >= re) return;
+        const int64_t o = static_cast<int64_t>(r) * N + c;
+        w[0] = ld_dep_v4(dH + o);
+        w[1] = ld_dep_v4(G + o);
+        w[2] = ld_dep_v4(U + o);
+      };
+      auto row = [&](int r, const uint4 (&w)[3]) {
+        const __half2* h2 = reinterpret_cast<const __half2*>(&w[0]);
+        const __half2* g2 = reinterpret_cast<const __half2*>(&w[1]);
+        const __half2* u2 = reinterpret_cast<const __half2*>(&w[2]);
+        uint4 og, ou;
+        __half2* og2 = reinterpret_cast<__half2*>(&og);
+        __half2* ou2 = reinterpret_cast<__half2*>(&ou);
 #pragma unroll
-        for (int q = 0; q < kUnroll; ++q) {
-          const int rq = r + 16 * q;
-          if (rq < re) {
-            const int64_t o = static_cast<int64_t>(rq) * N + c;
-            vh[q] = ld_dep_v4(dH + o);
-            vg[q] = ld_dep_v4(G + o);
-            vu[q] = ld_dep_v4(U + o);
-          }
+        for (int i = 0; i < 4; ++i) {
+          const float2 hv = __half22float2(h2[i]), gv = __half22float2(g2[i]), uv = __half22float2(u2[i]);
+          const F2 h = f2(hv.x, hv.y);
+          F2 fa, da;
+          act_fwd_bwd2<decltype(tag)::value>(f2(gv.x, gv.y), fa, da);
+          const F2 a = f2_mul(f2_mul(h, f2(uv.x, uv.y)), da), b = f2_mul(h, fa);
+          sg[i] = f2_add(sg[i], a);
+          su[i] = f2_add(su[i], b);
+          og2[i] = __float22half2_rn(f2_get(a));
+          ou2[i] = __float22half2_rn(f2_get(b));
         }
-#pragma unroll
-        for (int q = 0; q < kUnroll; ++q) {
-          const int rq = r + 16 * q;
-          if (rq >= re) break;
-          const __half2* h2 = reinterpret_cast<const __half2*>(&vh[q]);
-          const __half2* g2 = reinterpret_cast<const __half2*>(&vg[q]);
-          const __half2* u2 = reinterpret_cast<const __half2*>(&vu[q]);
-          uint4 og, ou;
-          __half2* og2 = reinterpret_cast<__half2*>(&og);
-          __half2* ou2 = reinterpret_cast<__half2*>(&ou);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 hv = __half22float2(h2[i]), gv = __half22float2(g2[i]), uv = __half22float2(u2[i]);
-            const F2 h = f2(hv.x, hv.y);
-            F2 fa, da;
-            act_fwd_bwd2<decltype(tag)::value>(f2(gv.x, gv.y), fa, da);
-            const F2 a = f2_mul(f2_mul(h, f2(uv.x, uv.y)), da), b = f2_mul(h, fa);
-            sg[i] = f2_add(sg[i], a);
-            su[i] = f2_add(su[i], b);
-            og2[i] = __float22half2_rn(f2_get(a));
-            ou2[i] = __float22half2_rn(f2_get(b));
-          }
-          const int64_t o = static_cast<int64_t>(rq) * N + c;
-          if (dG) {
-            *reinterpret_cast<uint4*>(dG + o) = og;
-            *reinterpret_cast<uint4*>(dU + o) = ou;
-          }
+        if (dG) {
+          const int64_t o = static_cast<int64_t>(r) * N + c;
+          *reinterpret_cast<uint4*>(dG + o) = og;
+          *reinterpret_cast<uint4*>(dU + o) = ou;
+        }
+      };
+      load(rb + ty, v[0]);
+      load(rb + ty + 16, v[1]);
+      for (int r = rb + ty; r < re; r += 32) {
+        row(r, v[0]);
+        load(r + 32, v[0]);
+        if (r + 16 < re) {
+          row(r + 16, v[1]);
+          load(r + 48, v[1]);
         }
       }
     });
