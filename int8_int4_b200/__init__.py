@@ -368,87 +368,92 @@ def qgemm_s32(Xq: torch.Tensor, Wq: torch.Tensor, out=None, stream=None):
 
 # --------------------------------------------------- feed-forward operators --
 
+_F16, _F32, _I8, _U8 = torch.float16, torch.float32, torch.int8, torch.uint8
+
+
 def _act(act: str) -> int:
     if act not in ACTS:
         raise ValueError(f"unknown activation {act!r}: one of {', '.join(ACTS)}")
     return ACTS[act]
 
 
-def _arg(t, name: str, shape: tuple, dtype, dev):
-    """Check one argument (None passes as NULL) and return its device pointer.
-    A call checks up to ten: the common outcome is one expression."""
+def _arg(t, name: str, shape: tuple, dtype, di: int):
+    """Check one argument (None passes as NULL) and return its device pointer;
+    `di` is the index of the call's CUDA device. A call checks up to ten: the
+    common outcome is one expression."""
     if t is None:
         return None
-    if t.shape == shape and t.dtype is dtype and t.device == dev and t.is_contiguous():
+    if t.shape == shape and t.dtype is dtype and t.get_device() == di and t.is_contiguous():
         return t.data_ptr()
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, the other arguments on {dev}")
+    if t.get_device() != di:
+        raise ValueError(f"{name} is on {t.device}, the other arguments on cuda:{di}")
     raise ValueError(f"{name} must be contiguous")
 
 
-def _weight_args(fmt: str, W, scales, sfx: str, N: int, K: int, dev):
+def _weight_args(fmt: str, W, scales, sfx: str, N: int, K: int, di: int):
     """Pointers of one packed weight [N,K] of the given format and its scales."""
     if fmt == "f16":
         if scales is not None:
             raise ValueError("f16 weights take no scales")
-        return _arg(W, "W" + sfx, (N, K), torch.float16, dev), None
+        return _arg(W, "W" + sfx, (N, K), _F16, di), None
     if scales is None:
         raise ValueError(f"{fmt} needs scales")
     if fmt == "q4":
         if K % 32:
             raise ValueError("q4 needs K % 32 == 0")
-        return (_arg(W, "W" + sfx, (N, K // 2), torch.uint8, dev),
-                _arg(scales, "scales" + sfx, (N, K // 32), torch.float16, dev))
-    return (_arg(W, "W" + sfx, (N, K), torch.int8, dev),
-            _arg(scales, "scales" + sfx, (N,), torch.float32, dev))
+        return (_arg(W, "W" + sfx, (N, K // 2), _U8, di),
+                _arg(scales, "scales" + sfx, (N, K // 32), _F16, di))
+    return (_arg(W, "W" + sfx, (N, K), _I8, di),
+            _arg(scales, "scales" + sfx, (N,), _F32, di))
 
 
 def _x_args(fmt: str, X, W, sx):
-    """Sizes and pointers of the activations: (M, N, K, X, sx)."""
+    """Sizes, device index and pointers of the activations: (M, N, K, di, X, sx)."""
     if fmt not in FORMATS:
         raise ValueError(f"unknown format {fmt!r}")
     if X.dim() != 2 or W.dim() != 2:
         raise ValueError("X and the weights must be 2-D")
-    if not X.is_cuda:
+    di = X.get_device()
+    if di < 0:
         raise ValueError("X must be a CUDA tensor (no CPU path exists)")
-    shape, dev = X.shape, X.device
+    shape = X.shape
     M, K = shape
     if fmt == "w8a8":
         if sx is None:
             raise ValueError("w8a8 needs sx")
-        px = _arg(X, "X", shape, torch.int8, dev)
-        sx = _arg(sx, "sx", (M,), torch.float32, dev)
+        px = _arg(X, "X", shape, _I8, di)
+        sx = _arg(sx, "sx", (M,), _F32, di)
     else:
         if sx is not None:
             raise ValueError("sx is for w8a8 only")
-        px = _arg(X, "X", shape, torch.float16, dev)
-    return M, W.shape[0], K, px, sx
+        px = _arg(X, "X", shape, _F16, di)
+    return M, W.shape[0], K, di, px, sx
 
 
-def _here(dev, stream):
+def _here(di: int, stream):
     """The current stream's handle where the call runs on it and on the current
     device, as almost every call does; None where _running_on is needed. (The
     handle without a Stream object: 0.1 instead of 3 us of a call's 9.)"""
-    if stream is None and dev.index == torch.cuda.current_device():
-        return torch._C._cuda_getCurrentRawStream(dev.index)
+    if stream is None and di == torch.cuda.current_device():
+        return torch._C._cuda_getCurrentRawStream(di)
     return None
 
 
 @contextlib.contextmanager
-def _running_on(dev, stream):
+def _running_on(di: int, stream):
     """Device and stream of one call: yields the stream's handle. With a stream
     of the caller's, tensors that the call allocates come from that stream's
     pool, so the memory is not still in use by work on another one."""
-    with torch.cuda.device(dev):
+    with torch.cuda.device(di):
         if stream is None:
-            yield torch._C._cuda_getCurrentRawStream(dev.index)
+            yield torch._C._cuda_getCurrentRawStream(di)
         else:
             s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(
-                _stream(stream), device=dev)
+                _stream(stream), device=di)
             with torch.cuda.stream(s):
                 yield s.cuda_stream
 
@@ -462,28 +467,31 @@ def qgemm_act(fmt: str, X: torch.Tensor, Wq: torch.Tensor, scales, sx=None, bias
     Formats and arguments as for qgemm; ``act`` is one of ACTS; ``residual``
     fp16 [M,N] may be ``out`` itself. With ``alpha_dev`` the strength is read
     from device memory and ``alpha`` is ignored."""
-    M, N, K, px, psx = _x_args(fmt, X, Wq, sx)
-    dev = X.device
-    pw, ps = _weight_args(fmt, Wq, scales, "", N, K, dev)
-    pb = _arg(bias, "bias", (N,), torch.float16, dev)
-    pr = _arg(residual, "residual", (M, N), torch.float16, dev)
-    pv = _arg(steer_vec, "steer_vec", (N,), torch.float32, dev)
-    if alpha_dev is not None and alpha_dev.numel() != 1:
+    M, N, K, di, px, psx = _x_args(fmt, X, Wq, sx)
+    pw, ps = _weight_args(fmt, Wq, scales, "", N, K, di)
+    mn, n = (M, N), (N,)
+    pb = _arg(bias, "bias", n, _F16, di)
+    pr = _arg(residual, "residual", mn, _F16, di)
+    pv = _arg(steer_vec, "steer_vec", n, _F32, di)
+    if alpha_dev is None:
+        pa = None
+    elif alpha_dev.numel() != 1:
         raise ValueError("alpha_dev must be one element")
-    pa = None if alpha_dev is None else _arg(alpha_dev, "alpha_dev", alpha_dev.shape, torch.float32, dev)
+    else:
+        pa = _arg(alpha_dev, "alpha_dev", alpha_dev.shape, _F32, di)
     a, g, f = _act(act), _group(fmt, group), FORMATS[fmt]
-    po = _arg(out, "out", (M, N), torch.float16, dev)
+    po = _arg(out, "out", mn, _F16, di)
     fn = load_library().aria_qgemm_act
-    raw = _here(dev, stream)
+    raw = _here(di, stream)
     if raw is not None:
         if out is None:
-            out = torch.empty(M, N, dtype=torch.float16, device=dev)
+            out = torch.empty(mn, dtype=_F16, device=X.device)
             po = out.data_ptr()
         st = fn(f, g, M, N, K, px, psx, pw, ps, pb, a, pr, pv, alpha, pa, po, raw)
     else:
-        with _running_on(dev, stream) as raw:
+        with _running_on(di, stream) as raw:
             if out is None:
-                out = torch.empty(M, N, dtype=torch.float16, device=dev)
+                out = torch.empty(mn, dtype=_F16, device=X.device)
                 po = out.data_ptr()
             st = fn(f, g, M, N, K, px, psx, pw, ps, pb, a, pr, pv, alpha, pa, po, raw)
     if st:
@@ -500,28 +508,30 @@ def qgemm_gated(fmt: str, X: torch.Tensor, Wg: torch.Tensor, scales_g, Wu: torch
     Both weights have one format and shape (as Wq and scales of qgemm; "f16"
     takes the fp16 weights and None for the scales). ``save`` = (G, U): fp16
     [M,N] tensors that receive g and u, for gated_backward."""
-    M, N, K, px, psx = _x_args(fmt, X, Wg, sx)
-    dev = X.device
-    pg, psg = _weight_args(fmt, Wg, scales_g, "g", N, K, dev)
-    pu, psu = _weight_args(fmt, Wu, scales_u, "u", N, K, dev)
-    pbg = _arg(bias_g, "bias_g", (N,), torch.float16, dev)
-    pbu = _arg(bias_u, "bias_u", (N,), torch.float16, dev)
-    G, U = (None, None) if save is None else save
-    pG = _arg(G, "save[0]", (M, N), torch.float16, dev)
-    pU = _arg(U, "save[1]", (M, N), torch.float16, dev)
+    M, N, K, di, px, psx = _x_args(fmt, X, Wg, sx)
+    pg, psg = _weight_args(fmt, Wg, scales_g, "g", N, K, di)
+    pu, psu = _weight_args(fmt, Wu, scales_u, "u", N, K, di)
+    mn, n = (M, N), (N,)
+    pbg = _arg(bias_g, "bias_g", n, _F16, di)
+    pbu = _arg(bias_u, "bias_u", n, _F16, di)
+    if save is None:
+        pG = pU = None
+    else:
+        pG = _arg(save[0], "save[0]", mn, _F16, di)
+        pU = _arg(save[1], "save[1]", mn, _F16, di)
     a, gr, f = _act(act), _group(fmt, group), FORMATS[fmt]
-    po = _arg(out, "out", (M, N), torch.float16, dev)
+    po = _arg(out, "out", mn, _F16, di)
     fn = load_library().aria_qgemm_gated
-    raw = _here(dev, stream)
+    raw = _here(di, stream)
     if raw is not None:
         if out is None:
-            out = torch.empty(M, N, dtype=torch.float16, device=dev)
+            out = torch.empty(mn, dtype=_F16, device=X.device)
             po = out.data_ptr()
         st = fn(f, gr, M, N, K, px, psx, pg, psg, pu, psu, pbg, pbu, a, po, pG, pU, raw)
     else:
-        with _running_on(dev, stream) as raw:
+        with _running_on(di, stream) as raw:
             if out is None:
-                out = torch.empty(M, N, dtype=torch.float16, device=dev)
+                out = torch.empty(mn, dtype=_F16, device=X.device)
                 po = out.data_ptr()
             st = fn(f, gr, M, N, K, px, psx, pg, psg, pu, psu, pbg, pbu, a, po, pG, pU, raw)
     if st:
@@ -548,12 +558,12 @@ def gated_backward(dH: torch.Tensor, X, Wg, Wu, G: torch.Tensor, U: torch.Tensor
     weight gradients only and the weights for dX only; K comes from either."""
     if dH.dim() != 2:
         raise ValueError("dH must be 2-D")
-    if not dH.is_cuda:
+    di = dH.get_device()
+    if di < 0:
         raise ValueError("dH must be a CUDA tensor (no CPU path exists)")
     if not (input_grad or weight_grad or bias_grad):
         raise ValueError("no gradient is asked for")
     M, N = dH.shape
-    dev = dH.device
     src = X if X is not None else Wg
     if src is None:
         if input_grad or weight_grad:
@@ -563,17 +573,17 @@ def gated_backward(dH: torch.Tensor, X, Wg, Wu, G: torch.Tensor, U: torch.Tensor
         raise ValueError("X and the weights must be 2-D")
     else:
         K = src.shape[1]
-    f16 = torch.float16
     if input_grad and (Wg is None or Wu is None):
         raise ValueError("dX needs Wg and Wu")
     if weight_grad and X is None:
         raise ValueError("dWg and dWu need X")
-    pin = (_arg(dH, "dH", (M, N), f16, dev), _arg(G, "G", (M, N), f16, dev), _arg(U, "U", (M, N), f16, dev),
-           _arg(X, "X", (M, K), f16, dev), _arg(Wg, "Wg", (N, K), f16, dev), _arg(Wu, "Wu", (N, K), f16, dev))
+    mn, mk, nk = (M, N), (M, K), (N, K)
+    pin = (_arg(dH, "dH", mn, _F16, di), _arg(G, "G", mn, _F16, di), _arg(U, "U", mn, _F16, di),
+           _arg(X, "X", mk, _F16, di), _arg(Wg, "Wg", nk, _F16, di), _arg(Wu, "Wu", nk, _F16, di))
     if pin[1] is None or pin[2] is None:
         raise ValueError("G and U are needed (qgemm_gated's save=)")
     a = _act(act)
-    shapes = ((M, K), (N, K), (N, K), (N,), (N,))
+    shapes = (mk, nk, nk, (N,), (N,))
     asked = (input_grad, weight_grad, weight_grad, bias_grad, bias_grad)
     names = ("dX", "dWg", "dWu", "dbg", "dbu")
     if out is not None:
@@ -582,22 +592,22 @@ def gated_backward(dH: torch.Tensor, X, Wg, Wu, G: torch.Tensor, U: torch.Tensor
         for t, on, n, sh in zip(out, asked, names, shapes):
             if (t is not None) != on:
                 raise ValueError(f"out: {n} is {'needed' if on else 'not asked for'}")
-            _arg(t, n, sh, f16, dev)
+            _arg(t, n, sh, _F16, di)
     need = gated_backward_workspace_size(M, N, K)
     if workspace is not None:
-        _arg(workspace, "workspace", workspace.shape, torch.uint8, dev)
+        _arg(workspace, "workspace", workspace.shape, _U8, di)
         if workspace.numel() < need:
             raise ValueError(f"workspace of {workspace.numel()} bytes, {need} needed")
     lib = load_library()
-    raw = _here(dev, stream)
-    with contextlib.nullcontext(raw) if raw is not None else _running_on(dev, stream) as raw:
+    raw = _here(di, stream)
+    with contextlib.nullcontext(raw) if raw is not None else _running_on(di, stream) as raw:
+        dev = dH.device
         if out is None:
-            dX = torch.empty_like(X) if input_grad and X is not None else (
-                torch.empty(M, K, dtype=f16, device=dev) if input_grad else None)
-            dWg, dWu = torch.empty((2, N, K), dtype=f16, device=dev).unbind() if weight_grad else (None, None)
-            dbg, dbu = torch.empty((2, N), dtype=f16, device=dev).unbind() if bias_grad else (None, None)
+            dX = torch.empty(mk, dtype=_F16, device=dev) if input_grad else None
+            dWg, dWu = torch.empty((2, N, K), dtype=_F16, device=dev).unbind() if weight_grad else (None, None)
+            dbg, dbu = torch.empty((2, N), dtype=_F16, device=dev).unbind() if bias_grad else (None, None)
             out = (dX, dWg, dWu, dbg, dbu)
-        ws = workspace if workspace is not None else torch.empty(need, dtype=torch.uint8, device=dev)
+        ws = workspace if workspace is not None else torch.empty(need, dtype=_U8, device=dev)
         _check(lib.aria_gated_bwd(a, M, N, K, *pin, *[None if t is None else t.data_ptr() for t in out],
                                   ws.data_ptr(), ws.numel(), raw))
     return tuple(out)

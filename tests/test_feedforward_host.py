@@ -119,6 +119,7 @@ def meta(*s, dtype=torch.float16):
     class T:
         shape, device, is_cuda = torch.Size(s), torch.device("cuda:0"), True
         dim = staticmethod(lambda: len(s))
+        get_device = staticmethod(lambda: 0)
         numel = staticmethod(lambda: torch.Size(s).numel())
         is_contiguous = staticmethod(lambda: True)
         data_ptr = staticmethod(lambda: A)
@@ -148,6 +149,7 @@ def test_binding_refuses_strides_and_other_devices():
         aq.qgemm_act("f16", meta(4, 64), meta(32, 64), None, residual=t)
     t = meta(4, 32)
     type(t).device = torch.device("cuda:1")
+    type(t).get_device = staticmethod(lambda: 1)
     with pytest.raises(ValueError, match="cuda:1"):
         aq.qgemm_act("f16", meta(4, 64), meta(32, 64), None, residual=t)
 
