@@ -417,6 +417,7 @@ struct SmallPlan {
 
 constexpr int64_t kSmallMaxTokens = 16;
 constexpr size_t kSmallSmemBudget = 110 * 1024;  // two CTAs per SM
+constexpr size_t kSmallSmemMost = 220 * 1024;    // one
 
 template <int KIND, int TB, int CH, int GP, int EPI>
 int small_max_clusters(int size, size_t smem) {
@@ -480,7 +481,11 @@ bool small_layout(int kind, int64_t M, int64_t N, int64_t K, int S, int clusters
   p->off_sw = p->off_bar + 16;  // q8 channel scales of the rows
   *smem = p->off_sw + static_cast<uint64_t>(rmax) * 4;
   (void)M;
-  return *smem <= kSmallSmemBudget;
+  // Two CTAs per SM: the next launch's weights stream beside this one. The
+  // gated operator's weights may be too many for that and still stream faster
+  // one CTA per SM than through the tensor-core kernel (q8, 6144 x 1536, one
+  // token: 6.0 against 10.1 us).
+  return *smem <= (rpc == 2 ? kSmallSmemMost : kSmallSmemBudget);
 }
 
 template <int KIND, int TB, int CH, int GP, int EPI>
@@ -523,15 +528,20 @@ bool plan_small_t(int64_t M, int64_t N, int64_t K, SmallPlan* out) {
   return true;
 }
 
+// 16-row groups per pass for one token block: a gated channel has two rows
+template <int EPI>
+constexpr int small_groups() { return EPI == aria::kEpiGated ? 6 : 4; }
+
 template <int EPI>
 bool plan_small(int kind, int64_t M, int64_t N, int64_t K, SmallPlan* out) {
   using namespace aria;
   if (M > kSmallMaxTokens) return false;
   const bool two = M > 8;
+  constexpr int gp = small_groups<EPI>();
   switch (kind) {
-    case kQ8: return two ? plan_small_t<kQ8, 2, 4, 2, EPI>(M, N, K, out) : plan_small_t<kQ8, 1, 6, 4, EPI>(M, N, K, out);
-    case kQ4: return two ? plan_small_t<kQ4, 2, 4, 2, EPI>(M, N, K, out) : plan_small_t<kQ4, 1, 6, 4, EPI>(M, N, K, out);
-    case kF16: return two ? plan_small_t<kF16, 2, 4, 2, EPI>(M, N, K, out) : plan_small_t<kF16, 1, 6, 4, EPI>(M, N, K, out);
+    case kQ8: return two ? plan_small_t<kQ8, 2, 4, 2, EPI>(M, N, K, out) : plan_small_t<kQ8, 1, 6, gp, EPI>(M, N, K, out);
+    case kQ4: return two ? plan_small_t<kQ4, 2, 4, 2, EPI>(M, N, K, out) : plan_small_t<kQ4, 1, 6, gp, EPI>(M, N, K, out);
+    case kF16: return two ? plan_small_t<kF16, 2, 4, 2, EPI>(M, N, K, out) : plan_small_t<kF16, 1, 6, gp, EPI>(M, N, K, out);
   }
   return false;
 }
@@ -566,14 +576,19 @@ aria_status launch_small_t(const SmallPlan& pl, cudaStream_t st) {
   return ARIA_OK;
 }
 
+template <int KIND, int EPI>
+aria_status launch_small_kind(const SmallPlan& pl, cudaStream_t st) {
+  return pl.tb == 2 ? launch_small_t<KIND, 2, 4, 2, EPI>(pl, st)
+                    : launch_small_t<KIND, 1, 6, small_groups<EPI>(), EPI>(pl, st);
+}
+
 template <int EPI>
 aria_status launch_small(int kind, const SmallPlan& pl, cudaStream_t st) {
   using namespace aria;
-  const bool two = pl.tb == 2;
   switch (kind) {
-    case kQ8: return two ? launch_small_t<kQ8, 2, 4, 2, EPI>(pl, st) : launch_small_t<kQ8, 1, 6, 4, EPI>(pl, st);
-    case kQ4: return two ? launch_small_t<kQ4, 2, 4, 2, EPI>(pl, st) : launch_small_t<kQ4, 1, 6, 4, EPI>(pl, st);
-    case kF16: return two ? launch_small_t<kF16, 2, 4, 2, EPI>(pl, st) : launch_small_t<kF16, 1, 6, 4, EPI>(pl, st);
+    case kQ8: return launch_small_kind<kQ8, EPI>(pl, st);
+    case kQ4: return launch_small_kind<kQ4, EPI>(pl, st);
+    case kF16: return launch_small_kind<kF16, EPI>(pl, st);
   }
   return fail(ARIA_ERR_INVALID_ARG, "unknown kind");
 }

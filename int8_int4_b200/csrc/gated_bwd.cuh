@@ -27,7 +27,7 @@ namespace aria {
 constexpr int kGbThreads = 256;
 constexpr int kGbCols = 128;
 
-__global__ void __launch_bounds__(kGbThreads, 4)
+__global__ void __launch_bounds__(kGbThreads, 3)
     gated_bwd_kernel(const __half* __restrict__ dH, const __half* __restrict__ G, const __half* __restrict__ U,
                      __half* __restrict__ dG, __half* __restrict__ dU, float* __restrict__ part, int M, int N,
                      int rows, int act) {

@@ -168,6 +168,18 @@ __device__ __forceinline__ void load_w16(const uint8_t* rowp, int kc, int q, uin
   }
 }
 
+template <int N>
+struct IntTag {
+  static constexpr int value = N;
+};
+
+// f(IntTag<n>) for a run-time n in [1, N]
+template <int N, class F>
+__device__ __forceinline__ void up_to(int n, F&& f) {
+  if (n == N) f(IntTag<N>{});
+  else if constexpr (N > 1) up_to<N - 1>(n, f);
+}
+
 // TB token blocks of 8 (M <= 8: 1; M <= 16: 2); CH: K chunks per warp held in
 // registers (the planner keeps kslice / 64 / 8 <= CH); GP: 16-row groups
 // accumulated in registers per pass over the chunks.
@@ -278,50 +290,46 @@ __global__ void __launch_bounds__(kSmThreads, 2) smallm_kernel(const SmallParams
       for (int tb = 0; tb < TB; ++tb)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[gi][tb][e] = 0.0f;
+    // The products of the pass's NG groups. The loop over the groups has no
+    // branch: their loads, conversions and MMAs then interleave, which is what
+    // the time of the dequantising formats depends on (6144 x 1536, one
+    // token, against a loop that leaves at the last group: q4 3.5 against 5.0
+    // us, gated q4 6.0 against 8.4, q8 2.8 against 4.0; fp16 unchanged). Rows
+    // beyond the last read that one again; their sums are not stored.
+    auto products = [&](auto ng) {
+      constexpr int NG = decltype(ng)::value;
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const int c = warp + i * kSmWarps;
-      if (c >= nch) break;
+      for (int i = 0; i < CH; ++i) {
+        const int c = warp + i * kSmWarps;
+        if (c >= nch) break;
 #pragma unroll
-      for (int gi = 0; gi < GP; ++gi) {
-        const int g = gp + gi;
-        if (g >= groups) break;
-        const int ra = g * 16 + g4, rb = ra + 8;
-        uint32_t ha[8], hb[8];
-        uint32_t sa = 0u, sb = 0u;
-        if constexpr (KIND == kQ4) {
-          // this lane's 16 k values lie in group (64c + 16q) / 32 of the slice
-          const int gi32 = c * 2 + (q >> 1);
-          const uint16_t va = ra < R ? __half_as_ushort(scs[ra * (p.kslice / 32) + gi32]) : 0;
-          const uint16_t vb = rb < R ? __half_as_ushort(scs[rb * (p.kslice / 32) + gi32]) : 0;
-          sa = static_cast<uint32_t>(va) * 0x10001u;
-          sb = static_cast<uint32_t>(vb) * 0x10001u;
-        }
-        if (ra < R) {
+        for (int gi = 0; gi < NG; ++gi) {
+          const int ra = min((gp + gi) * 16 + g4, R - 1), rb = min((gp + gi) * 16 + g4 + 8, R - 1);
+          uint32_t ha[8], hb[8];
+          uint32_t sa = 0u, sb = 0u;
+          if constexpr (KIND == kQ4) {
+            // this lane's 16 k values lie in group (64c + 16q) / 32 of the slice
+            const int gi32 = c * 2 + (q >> 1);
+            sa = __half_as_ushort(scs[ra * (p.kslice / 32) + gi32]) * 0x10001u;
+            sb = __half_as_ushort(scs[rb * (p.kslice / 32) + gi32]) * 0x10001u;
+          }
           load_w16<KIND>(wsm + ra * p.wrow, c, q, sa, ha);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) ha[e] = 0u;
-        }
-        if (rb < R) {
           load_w16<KIND>(wsm + rb * p.wrow, c, q, sb, hb);
-        } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) hb[e] = 0u;
-        }
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t a[4] = {ha[2 * j], hb[2 * j], ha[2 * j + 1], hb[2 * j + 1]};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t a[4] = {ha[2 * j], hb[2 * j], ha[2 * j + 1], hb[2 * j + 1]};
-#pragma unroll
-          for (int tb = 0; tb < TB; ++tb) {
-            const uint4& x = j < 2 ? xa[i][tb] : xb[i][tb];
-            const uint32_t b0 = (j & 1) ? x.z : x.x;
-            const uint32_t b1 = (j & 1) ? x.w : x.y;
-            mma_16816(acc[gi][tb], a, b0, b1);
+            for (int tb = 0; tb < TB; ++tb) {
+              const uint4& x = j < 2 ? xa[i][tb] : xb[i][tb];
+              const uint32_t b0 = (j & 1) ? x.z : x.x;
+              const uint32_t b1 = (j & 1) ? x.w : x.y;
+              mma_16816(acc[gi][tb], a, b0, b1);
+            }
           }
         }
       }
-    }
+    };
+    up_to<GP>(min(groups - gp, GP), products);
     // partial sums of this pass: red[warp][token][row]
     __syncthreads();  // the previous pass's reduction has read red
 #pragma unroll
