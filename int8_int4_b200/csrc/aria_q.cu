@@ -1153,7 +1153,7 @@ TgChoice choose_tg(bool gated, int64_t M, int64_t N, int64_t nkb) {
 // 18.4 against 17.6.
 bool use_tg(int kind, bool gated, int64_t M, int64_t N, int64_t K, int* bn) {
   using namespace aria;
-  if ((kind != kF16 && kind != kW8A8) || M < 128) return false;
+  if ((kind != kF16 && kind != kW8A8) || M < 128 || M > (1 << 30)) return false;  // (row indices: 32 bits)
   const int64_t nkb = (K * (kind == kF16 ? 2 : 1) + 127) / 128;
   const TgChoice tg = choose_tg(gated, M, N, nkb);
   *bn = tg.bn;
@@ -1242,7 +1242,7 @@ int64_t bwd_makespan(int units, int64_t n0, int64_t l0, int64_t n1, int64_t l1, 
 }
 
 struct BwdPlan {
-  int rows = 16, P = 1;   // rows per block of the elementwise kernel, blocks along M
+  int rows = 32, P = 1;   // rows per block of the elementwise kernel, blocks along M
   int parts = 1;          // shares of a dX tile's k
   int units = 1;
   aria::TgSched sched{};
@@ -1252,8 +1252,9 @@ BwdPlan make_bwd_plan(int64_t M, int64_t N, int64_t K, bool dx, bool dw, int uni
   using namespace aria;
   BwdPlan pl;
   // at most 64 partials per column (their sum is read once more), and at
-  // least 16 rows per block, one per row lane
-  pl.rows = static_cast<int>(std::max<int64_t>(16, ((M + 63) / 64 + 15) / 16 * 16));
+  // least 32 rows per block, two for each of its 16 row lanes, whose loads
+  // are then in flight together
+  pl.rows = static_cast<int>(std::max<int64_t>(32, ((M + 63) / 64 + 15) / 16 * 16));
   pl.P = static_cast<int>((M + pl.rows - 1) / pl.rows);
   auto tiles = [](int64_t rows, int64_t cols) {
     return (rows + 2 * kTgRows - 1) / (2 * kTgRows) * ((cols + kBwdBn - 1) / kBwdBn);
@@ -1309,7 +1310,8 @@ BwdPlan bwd_plan(int64_t M, int64_t N, int64_t K, bool dx, bool dw) {
 // keeps every byte count below 2^48 (no device holds such tensors)
 aria_status check_bwd_size(int64_t M, int64_t N, int64_t K) {
   constexpr int64_t kMost = int64_t{1} << 40;
-  if (N > kMaxDim / 2) return fail(ARIA_ERR_UNSUPPORTED, "gated: N must be below 2^30");
+  if (N > kMaxDim / 2 || M > kMaxDim / 2 || K > kMaxDim / 2)
+    return fail(ARIA_ERR_UNSUPPORTED, "gated backward: sizes must be below 2^30");
   if (M > kMost / N || M > kMost / K || N > kMost / K)
     return fail(ARIA_ERR_UNSUPPORTED, "gated backward: a tensor of 2^40 elements or more");
   return ARIA_OK;
@@ -1458,24 +1460,16 @@ ARIA_API aria_status aria_gated_bwd(aria_act act, int64_t M, int64_t N, int64_t 
   __half* dG = (dX || dWg) ? reinterpret_cast<__half*>(ws) : nullptr;
   __half* dU = (dX || dWg) ? reinterpret_cast<__half*>(ws + l.off_du) : nullptr;
   float* part = dbg ? reinterpret_cast<float*>(ws + l.off_part) : nullptr;
-  {
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attr[1];
-    cfg.stream = st;
-    cfg.gridDim = dim3(static_cast<unsigned>((N + kGbCols - 1) / kGbCols), static_cast<unsigned>(bp.P));
-    cfg.blockDim = dim3(kGbThreads);
-    set_pdl(cfg, attr);
-    cudaError_t e = cudaLaunchKernelEx(&cfg, gated_bwd_kernel, static_cast<const __half*>(dH),
-                                       static_cast<const __half*>(G), static_cast<const __half*>(U), dG, dU, part,
-                                       static_cast<int>(M), static_cast<int>(N), bp.rows, static_cast<int>(act));
-    if (e != cudaSuccess) return cuda_fail(e, "gated backward launch");
-  }
   // the column sums are added by idle warps of the products' launch, or, where
   // a last launch is needed anyway, by that one
   const bool finish = bp.parts > 1 || (!dX && !dWg);
   float* xpart = reinterpret_cast<float*>(ws + l.off_x);
+  const int64_t count = bp.parts > 1 ? M * K : 0;
+  const int64_t nb = part ? (2 * N + 63) / 64 : 0, nx = (count / 4 + 255) / 256;
+  if (nb + nx > kMaxDim) return fail(ARIA_ERR_UNSUPPORTED, "too many elements");
+  // everything that can be refused comes before the first launch
+  TgPlan pl;
   if (dX || dWg) {
-    TgPlan pl;
     if ((s = plan_tg(true, kBwdBn, &pl)) != ARIA_OK) return s;
     pl.p.sched = bp.sched;
     pl.p.nunit = bp.units;
@@ -1501,12 +1495,21 @@ ARIA_API aria_status aria_gated_bwd(aria_act act, int64_t M, int64_t N, int64_t 
       if ((s = out_map(&pl.m.D[1], dWg, N, K)) != ARIA_OK) return s;
       if ((s = out_map(&pl.m.D[2], dWu, N, K)) != ARIA_OK) return s;
     }
-    if ((s = launch_tg<kTgGrad, false>(pl, st)) != ARIA_OK) return s;
   }
+  {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    cfg.stream = st;
+    cfg.gridDim = dim3(static_cast<unsigned>((N + kGbCols - 1) / kGbCols), static_cast<unsigned>(bp.P));
+    cfg.blockDim = dim3(kGbThreads);
+    set_pdl(cfg, attr);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, gated_bwd_kernel, static_cast<const __half*>(dH),
+                                       static_cast<const __half*>(G), static_cast<const __half*>(U), dG, dU, part,
+                                       static_cast<int>(M), static_cast<int>(N), bp.rows, static_cast<int>(act));
+    if (e != cudaSuccess) return cuda_fail(e, "gated backward launch");
+  }
+  if ((dX || dWg) && (s = launch_tg<kTgGrad, false>(pl, st)) != ARIA_OK) return s;
   if (finish) {
-    const int64_t count = bp.parts > 1 ? M * K : 0;
-    const int64_t nb = part ? (2 * N + 255) / 256 : 0, nx = (count / 4 + 255) / 256;
-    if (nb + nx > kMaxDim) return fail(ARIA_ERR_UNSUPPORTED, "too many elements");
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
     cfg.stream = st;

@@ -107,9 +107,10 @@ __global__ void __launch_bounds__(kGbThreads, 3)
 }
 
 // The end of a call whose products could not finish everything themselves:
-// the column partials' sums (`part`, P rows of [2 n]; blocks 0 .. nb - 1) and
-// dX from the S fp32 partials [S][count] of its split k (the blocks behind
-// them). Both are added in order.
+// the column partials' sums (`part`, P rows of [2 n]; blocks 0 .. nb - 1, 64
+// columns each, four threads per column so that all of its at most 64 loads
+// are in flight at once) and dX from the S fp32 partials [S][count] of its
+// split k (the blocks behind them). Both are added in a fixed order.
 __global__ void __launch_bounds__(256)
     bwd_finish_kernel(const float* __restrict__ part, __half* __restrict__ db0, __half* __restrict__ db1, int P,
                       int n, int nb, const float* __restrict__ xpart, __half* __restrict__ dX, int S,
@@ -117,13 +118,21 @@ __global__ void __launch_bounds__(256)
   pdl_wait();
   pdl_launch_dependents();
   if (static_cast<int>(blockIdx.x) < nb) {
-    const int c = blockIdx.x * 256 + threadIdx.x;
-    if (c >= 2 * n) return;
+    __shared__ float quarter[4][64];
+    const int cc = threadIdx.x & 63, qr = threadIdx.x >> 6;
+    const int c = blockIdx.x * 64 + cc;
     float s = 0.0f;
-#pragma unroll 8
-    for (int i = 0; i < P; ++i) s += ld_dep_f32(part + static_cast<int64_t>(i) * 2 * n + c);
-    if (c < n) db0[c] = __float2half_rn(s);
-    else db1[c - n] = __float2half_rn(s);
+    if (c < 2 * n) {
+#pragma unroll 16
+      for (int i = qr; i < P; i += 4) s += ld_dep_f32(part + static_cast<int64_t>(i) * 2 * n + c);
+    }
+    quarter[qr][cc] = s;
+    __syncthreads();
+    if (qr == 0 && c < 2 * n) {
+      const __half h = __float2half_rn((quarter[0][cc] + quarter[1][cc]) + (quarter[2][cc] + quarter[3][cc]));
+      if (c < n) db0[c] = h;
+      else db1[c - n] = h;
+    }
     return;
   }
   const int64_t e = (static_cast<int64_t>(blockIdx.x - nb) * 256 + threadIdx.x) * 4;  // count % 16 == 0

@@ -430,17 +430,25 @@ __global__ void __launch_bounds__(kTgThreads, 1)
     }
   } else if (warp < 4) {
     // --------------------------------- column sums of an earlier kernel
-    // One thread per output, the partials in order; their loads are
-    // independent, so eight are in flight.
+    // One thread per output; four interleaved sums, joined as
+    // bwd_finish_kernel joins its four threads', so that either gives the same
+    // bytes.
     if (MODE == kTgGrad && p.colsum.part) {
       const ColSum& cs = p.colsum;
       const int n2 = 2 * cs.n;
       for (int c = static_cast<int>(blockIdx.x) * 64 + (warp - 2) * 32 + lane; c < n2;
            c += static_cast<int>(gridDim.x) * 64) {
-        float sum = 0.0f;
-#pragma unroll 8
-        for (int i = 0; i < cs.P; ++i) sum += ld_dep_f32(cs.part + static_cast<int64_t>(i) * n2 + c);
-        const __half h = __float2half_rn(sum);
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        const float* pc = cs.part + c;
+        int i = 0;
+        for (; i + 4 <= cs.P; i += 4) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) sum[q] += ld_dep_f32(pc + static_cast<int64_t>(i + q) * n2);
+        }
+#pragma unroll
+        for (int q = 0; q < 3; ++q)
+          if (i + q < cs.P) sum[q] += ld_dep_f32(pc + static_cast<int64_t>(i + q) * n2);
+        const __half h = __float2half_rn((sum[0] + sum[1]) + (sum[2] + sum[3]));
         if (c < cs.n) cs.out0[c] = h;
         else cs.out1[c - cs.n] = h;
       }

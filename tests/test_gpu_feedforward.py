@@ -312,16 +312,23 @@ def test_backward_against_differences(act):
 
 @pytest.mark.parametrize("want", [w for w in itertools.product((True, False), repeat=3) if any(w)])
 def test_backward_parts(want):
-    """Each subset of the gradients is what the full call gives."""
-    dH, X, Wg, Wu, G, U = bwd_inputs(77, 144, 208)
-    full = aq.gated_backward(dH, X, Wg, Wu, G, U)
+    """Each subset of the gradients is what the full call gives: the same bytes,
+    but for dX, whose sum over the channels may be divided differently (fp32
+    sums that differ by their order, then one rounding: one step of fp16, of
+    the sum's largest partial sums where it cancels)."""
     i, w, b = want
-    part = aq.gated_backward(dH, X if w else None, Wg if i else None, Wu if i else None, G, U, input_grad=i,
-                             weight_grad=w, bias_grad=b)
-    for f, p, on in zip(full, part, (i, w, w, b, b)):
-        assert (p is None) == (not on)
-        if on:
-            assert torch.equal(f, p)
+    for M, N, K in ((77, 144, 208), (1300, 400, 272), (2100, 1040, 256)):
+        dH, X, Wg, Wu, G, U = bwd_inputs(M, N, K)
+        full = aq.gated_backward(dH, X, Wg, Wu, G, U)
+        part = aq.gated_backward(dH, X if w else None, Wg if i else None, Wu if i else None, G, U, input_grad=i,
+                                 weight_grad=w, bias_grad=b)
+        for k, (f, p, on) in enumerate(zip(full, part, (i, w, w, b, b))):
+            assert (p is None) == (not on)
+            if on and k:
+                assert torch.equal(f, p)
+            elif on:
+                slack = 2.0 ** -10 * f.double().abs() + 2.0 ** -24 + 2.0 ** -20 * f.double().abs().max()
+                assert ((f.double() - p.double()).abs() <= slack).all()
 
 
 def test_backward_workspace_needs_no_preparation():
@@ -426,3 +433,48 @@ def test_two_streams_at_once():
     for i in range(2):
         for g, h in got[i]:
             assert torch.equal(h, hs[i]) and all(torch.equal(a, b) for a, b in zip(g, refs[i]))
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements in X's, H's and the gradients' rows: the last
+    rows and columns against 64 bits (K is short: the size is in M N)."""
+    M, N, K = 70000, 32768, 64
+    assert M * N > 2 ** 31
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB of device memory")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    r = lambda *s, std=1.0: (torch.randn(*s, generator=g, device="cuda", dtype=torch.float16) * std)
+    X, Wg, Wu = r(M, K), r(N, K, std=0.1), r(N, K, std=0.1)
+    G, U = torch.empty(M, N, dtype=torch.float16, device="cuda"), torch.empty(M, N, dtype=torch.float16, device="cuda")
+    H = aq.qgemm_gated("f16", X, Wg, None, Wu, None, save=(G, U))
+    rows = slice(M - 70, M)
+    zg, dg = project(X[rows].double(), Wg.double(), None)
+    zu, du = project(X[rows].double(), Wu.double(), None)
+    a = act64(zg, "silu")
+    close(G[rows], zg, dg + H16 * zg.abs() + SUB)
+    close(U[rows], zu, du + H16 * zu.abs() + SUB)
+    close(H[rows], a * zu, zu.abs() * 1.13 * dg + a.abs() * du + 1.13 * dg * du + (2.0 ** -18 + H16) * (a * zu).abs() + SUB)
+    # in place on the residual: the whole of H is read and written
+    tail, last = H[rows].double(), Wg.double()
+    Wq, s = aq.qpack("q8", Wg)
+    aq.qgemm_act("q8", X, Wq, s, act="relu", residual=H, out=H)
+    z, dz = project(X[rows].double(), Wq.double() * s.double()[:, None], None)
+    y = z.clamp_min(0) + tail
+    close(H[rows], y, dz + 2.0 ** -18 * z.abs() + 2.0 ** -21 * (z.abs() + tail.abs()) + H16 * y.abs() + SUB)
+    del tail, last, z, dz, y, a, zg, zu, dg, du
+    dX, dWg, dWu, dbg, dbu = aq.gated_backward(H, X, Wg, Wu, G, U)
+    gg, gu = grads64(H[rows], G[rows], U[rows], "silu")
+    ref = gg @ Wg.double() + gu @ Wu.double()
+    s = gg.abs() @ Wg.double().abs() + gu.abs() @ Wu.double().abs()
+    # (the operands' rounding dominates: 2^-11 of every term, plus their evaluation)
+    close(dX[rows], ref, (H16 + 2.0 ** -17 + (2 * N / 16 + 16) * 2.0 ** -23) * s + H16 * ref.abs() + SUB * N)
+    cols = slice(N - 8, N)
+    gg, gu = grads64(H[:, cols].contiguous(), G[:, cols].contiguous(), U[:, cols].contiguous(), "silu")
+    for got, gw, d in ((dWg, dbg, gg), (dWu, dbu, gu)):
+        ref, s = d.t() @ X.double(), d.abs().t() @ X.double().abs()
+        fits = ref.abs() < 6e4  # sums over 70000 tokens may pass fp16's range
+        close(torch.where(fits, got[cols].double(), ref), ref,
+              (H16 + 2.0 ** -17 + (M / 16 + 16) * 2.0 ** -23) * s + H16 * ref.abs() + SUB * M)
+        fits = d.sum(0).abs() < 6e4
+        close(torch.where(fits, gw[cols].double(), d.sum(0)), d.sum(0),
+              (2.0 ** -17 + M * 2.0 ** -24) * d.abs().sum(0) + H16 * d.sum(0).abs() + SUB)
