@@ -4,9 +4,10 @@
 // All are written in a form that keeps its RELATIVE accuracy where the
 // result is small (negative z), because the result is rounded to fp16, whose
 // steps shrink with it: sigmoid products instead of 1 + tanh, and the
-// complementary error function's scaled form instead of 1 + erf. Measured on
-// the host in fp32 against 64 bits the largest relative error of any of them
-// is about 3e-6 for |z| <= 8, far below fp16's half step of 4.9e-4.
+// complementary error function's scaled form instead of 1 + erf. Measured
+// against 64 bits on a million points, |z| <= 8: largest relative error silu
+// 5e-7, gelu 3.3e-6, gelu_tanh 8e-6 (half a step of fp16 is 4.9e-4);
+// derivatives 2e-6 absolute.
 #pragma once
 
 #include <cuda_fp16.h>

@@ -140,6 +140,18 @@ def test_act_sizes(fmt, M, N, K):
     check_act(fmt, M, N, K, ACTS[i % 5], residual=i % 3 != 0 or ACTS[i % 5] == "none", steer=i % 2 == 0)
 
 
+# sizes where the linear runs on the token-major kernel, with tiles of 128, 192
+# and 256 columns, and odd edges of both rows and columns
+LARGE = [(4100, 1552, 2576), (3000, 1040, 6160), (1100, 6160, 2576)]
+
+
+@pytest.mark.parametrize("fmt", ["f16", "w8a8"])
+@pytest.mark.parametrize("M,N,K", LARGE)
+@pytest.mark.parametrize("act,residual,steer", [("gelu", True, True), ("silu", False, False), ("none", True, False)])
+def test_act_many_tokens(fmt, M, N, K, act, residual, steer):
+    check_act(fmt, M, N, K, act, residual, steer)
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("M", [5, 150])
@@ -160,7 +172,7 @@ def test_act_none_without_residual_is_the_plain_gemm(fmt, M, N, K):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
-@pytest.mark.parametrize("M,N,K", [(4, 256, 1024), (130, 1536, 6144), (500, 1536, 512), (1100, 512, 512)])
+@pytest.mark.parametrize("M,N,K", [(4, 256, 1024), (130, 1536, 6144), (500, 1536, 512), (1100, 6160, 2560)])
 def test_residual_in_place_and_strengths(fmt, M, N, K):
     X, sx, _ = acts(fmt, 1, M, K)
     W, s, _ = weight(fmt, 2, N, K)
@@ -210,6 +222,14 @@ def test_gated_sizes(fmt, M, N, K):
         K = (K + 255) // 256 * 256
     i = M + N + K
     check_gated(fmt, M, N, K, ACTS[i % 5], save=i % 2 == 0)
+
+
+@pytest.mark.parametrize("fmt", ["f16", "w8a8"])
+@pytest.mark.parametrize("M,N,K", [(130, 1040, 592), (300, 3088, 80), (1100, 1552, 80), (3000, 1040, 80)])
+@pytest.mark.parametrize("save", [False, True])
+def test_gated_tile_widths(fmt, M, N, K, save):
+    """Token-major tiles of 128, 192 and 256 columns with odd edges."""
+    check_gated(fmt, M, N, K, "gelu", save)
 
 
 @pytest.mark.parametrize("fmt", FMTS)
