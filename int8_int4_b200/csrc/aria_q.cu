@@ -484,8 +484,9 @@ bool small_layout(int kind, int64_t M, int64_t N, int64_t K, int S, int clusters
   // Two CTAs per SM: the next launch's weights stream beside this one. The
   // gated operator's weights may be too many for that and still stream faster
   // one CTA per SM than through the tensor-core kernel (q8, 6144 x 1536, one
-  // token: 6.0 against 10.1 us).
-  return *smem <= (rpc == 2 ? kSmallSmemMost : kSmallSmemBudget);
+  // token: 6.0 against 10.1 us), up to 8 tokens (16 tokens, 1536 x 6144: 11.8
+  // against 11.5).
+  return *smem <= (rpc == 2 && tb == 1 ? kSmallSmemMost : kSmallSmemBudget);
 }
 
 template <int KIND, int TB, int CH, int GP, int EPI>
