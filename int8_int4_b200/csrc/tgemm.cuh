@@ -483,8 +483,9 @@ __global__ void __launch_bounds__(kTgThreads, 1)
     // kTgAct: the residual of a unit is loaded by TMA into the box that will
     // carry the unit's result, kTgSlots - 1 units ahead and across items (the
     // lane reads its row of the box, adds, and writes the sum in its place).
-    // Read directly, 16 bytes per row and lane, it bounded the epilogue: 53-61
-    // us at M = 4096, N = 6144, K = 1536, W8A8.
+    // Read directly, 16 bytes per row and lane, it took longer: W8A8 with relu
+    // at M = 4096, N = 6144, K = 1536 49 against 44 us, the down projection 39
+    // against 38.
     TgItem pit;
     int pi = 0, pc = cg, pslot = 0;
     bool pvalid = valid;
