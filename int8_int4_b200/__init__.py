@@ -601,13 +601,9 @@ def gated_backward(dH: torch.Tensor, X, Wg, Wu, G: torch.Tensor, U: torch.Tensor
     lib = load_library()
     raw = _here(di, stream)
     with contextlib.nullcontext(raw) if raw is not None else _running_on(di, stream) as raw:
-        dev = dH.device
         if out is None:
-            dX = torch.empty(mk, dtype=_F16, device=dev) if input_grad else None
-            dWg, dWu = torch.empty((2, N, K), dtype=_F16, device=dev).unbind() if weight_grad else (None, None)
-            dbg, dbu = torch.empty((2, N), dtype=_F16, device=dev).unbind() if bias_grad else (None, None)
-            out = (dX, dWg, dWu, dbg, dbu)
-        ws = workspace if workspace is not None else torch.empty(need, dtype=_U8, device=dev)
+            out = tuple([dH.new_empty(sh) if on else None for on, sh in zip(asked, shapes)])
+        ws = workspace if workspace is not None else dH.new_empty(need, dtype=_U8)
         _check(lib.aria_gated_bwd(a, M, N, K, *pin, *[None if t is None else t.data_ptr() for t in out],
                                   ws.data_ptr(), ws.numel(), raw))
     return tuple(out)
