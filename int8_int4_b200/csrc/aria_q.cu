@@ -1220,6 +1220,7 @@ aria_status forward_tg(int kind, int bn, int64_t M, int64_t N, int64_t K, const 
 // from a 256-byte boundary.
 constexpr int kBwdBn = 256;        // columns of a gradient tile
 constexpr int kBwdMaxParts = 16;
+constexpr int kBwdItemMin = 9;     // K blocks' time that an item's epilogue takes: no item costs less
 
 // The longest time of a unit, in K blocks, when `units` pairs take n0 items of
 // length l0 first and then n1 <= l0 long ones; the caps go to *sc.
@@ -1261,7 +1262,7 @@ BwdPlan make_bwd_plan(int64_t M, int64_t N, int64_t K, bool dx, bool dw, int uni
     return (rows + 2 * kTgRows - 1) / (2 * kTgRows) * ((cols + kBwdBn - 1) / kBwdBn);
   };
   const int64_t tx = dx ? tiles(M, K) : 0, lx = 2 * ((N + 63) / 64);
-  const int64_t tw = dw ? 2 * tiles(N, K) : 0, lw = (M + 63) / 64;
+  const int64_t tw = dw ? 2 * tiles(N, K) : 0, lw = std::max<int64_t>(kBwdItemMin, (M + 63) / 64);
   // Shares of k for dX: each more than one costs a further launch that reads
   // the fp32 partials back, about 10 K blocks' time, and every partial is
   // written and read once more (a K block moves 64 KB per pair in 0.3 us;
@@ -1269,7 +1270,7 @@ BwdPlan make_bwd_plan(int64_t M, int64_t N, int64_t K, bool dx, bool dw, int uni
   int64_t best = -1;
   for (int s = 1; s <= kBwdMaxParts && s <= lx; ++s) {
     if (s > 1 && (!dx || tx * s > 4 * units)) break;
-    const int64_t l = (lx + s - 1) / s;
+    const int64_t l = std::max<int64_t>(kBwdItemMin, (lx + s - 1) / s);
     TgSched sc{};
     int64_t t;
     if (l >= lw || !dw) {
