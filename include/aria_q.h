@@ -193,7 +193,8 @@ aria_status aria_qgemm_steer_dev(aria_format fmt, int group, int64_t M, int64_t 
  * on the residual stream ("Steering is real").
  *   act        the activation; ARIA_ACT_NONE for none.
  *   residual   device fp16 [M,N], or NULL. May be Y itself (the add is then in
- *              place); any other overlap with Y is INVALID_ARG.
+ *              place); any other overlap with Y is INVALID_ARG, as is a Y
+ *              that overlaps X or the weights.
  *   steer_vec, alpha   as for aria_qgemm; alpha_dev, if not NULL, a device
  *              fp32 scalar (4-byte aligned) used instead of alpha, as in
  *              aria_qgemm_steer_dev (ignored without steer_vec). A strength of
@@ -223,7 +224,8 @@ aria_status aria_qgemm_act(aria_format fmt, int group, int64_t M, int64_t N, int
  *   H       device output fp16 [M,N].
  *   G, U    device outputs fp16 [M,N] that receive g and u, each rounded once
  *           (what aria_gated_bwd needs), or both NULL.
- *   H, G and U must not overlap one another (INVALID_ARG) nor any input.
+ *   H, G and U must not overlap one another, X or a weight (INVALID_ARG), nor
+ *   any other input.
  * g and u stay in fp32 up to the product; H is rounded once. Shape rules,
  * errors and stream order as for aria_qgemm; both weights are loaded before
  * the dependency wait. Deterministic; H does not depend on whether G and U

@@ -1033,6 +1033,15 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   return x < y + nb && y < x + na;
 }
 
+size_t x_bytes(int kind, int64_t M, int64_t K) {
+  return static_cast<size_t>(M) * K * (kind == aria::kW8A8 ? 1 : 2);
+}
+
+size_t weight_bytes(int kind, int64_t N, int64_t K) {
+  const size_t nk = static_cast<size_t>(N) * K;
+  return kind == aria::kF16 ? nk * 2 : kind == aria::kQ4 ? nk / 2 : nk;
+}
+
 // ---- the token-major kernel's plan and launch
 struct TgPlan {
   aria::TgParams p;
@@ -1352,6 +1361,8 @@ ARIA_API aria_status aria_qgemm_act(aria_format fmt, int group, int64_t M, int64
   const size_t yb = static_cast<size_t>(M) * N * 2;
   if (residual != Y && overlap(residual, yb, Y, yb))
     return fail(ARIA_ERR_INVALID_ARG, "the residual may be Y itself, but not overlap it otherwise");
+  if (overlap(X, x_bytes(kind, M, K), Y, yb) || overlap(Wq, weight_bytes(kind, N, K), Y, yb))
+    return fail(ARIA_ERR_INVALID_ARG, "Y overlaps X or the weights");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (!steer_vec) alpha_dev = nullptr;
   if (act == ARIA_ACT_NONE && !residual)  // the plain GEMM, byte for byte
@@ -1385,6 +1396,10 @@ ARIA_API aria_status aria_qgemm_gated(aria_format fmt, int group, int64_t M, int
   const size_t yb = static_cast<size_t>(M) * N * 2;
   if (overlap(G, yb, U, yb) || overlap(G, yb, H, yb) || overlap(U, yb, H, yb))
     return fail(ARIA_ERR_INVALID_ARG, "H, G and U must not overlap");
+  for (const void* o : {static_cast<const void*>(H), static_cast<const void*>(G), static_cast<const void*>(U)})
+    if (overlap(X, x_bytes(kind, M, K), o, yb) || overlap(Wg, weight_bytes(kind, N, K), o, yb) ||
+        overlap(Wu, weight_bytes(kind, N, K), o, yb))
+      return fail(ARIA_ERR_INVALID_ARG, "an output overlaps X or a weight");
   EpiArgs ea;
   ea.act = act;
   ea.Wu = Wu;

@@ -48,7 +48,7 @@ def bwd(lib, a=2, M=4, N=32, K=64, dh=DH, g=G, u=U, x=X, wg=W, wu=WU, dx=DX, dwg
     (dict(r=BAD), 3), (dict(y=BAD), 3), (dict(v=BAD), 3), (dict(v=V, ad=P(A + 2)), 3),
     (dict(M=0), 1), (dict(N=24), 2), (dict(K=24), 2), (dict(fmt=2, group=32, s=S, K=128), 2),
     (dict(fmt=2, group=16, s=S, K=256), 2), (dict(fmt=3, s=S, sx=SX, K=133152), 2), (dict(M=2 ** 31), 1),
-    (dict(r=P(Y.value + 16)), 1), (dict(r=P(Y.value - 4 * 32 * 2 + 16)), 1),
+    (dict(y=X), 1), (dict(y=W), 1), (dict(y=P(X.value + 4 * 64 * 2 - 16)), 1), (dict(r=P(Y.value + 16)), 1), (dict(r=P(Y.value - 4 * 32 * 2 + 16)), 1),
 ])
 def test_act_refusals(lib, kw, status):
     assert act(lib, **kw) == status
@@ -58,6 +58,7 @@ def test_act_refusals(lib, kw, status):
 @pytest.mark.parametrize("kw,status", [
     (dict(x=None), 1), (dict(wg=None), 1), (dict(wu=None), 1), (dict(h=None), 1),
     (dict(a=7), 1), (dict(fmt=0), 1), (dict(fmt=1, sg=S), 1), (dict(fmt=1, su=SU), 1), (dict(sg=S), 1), (dict(su=SU), 1),
+    (dict(h=X), 1), (dict(h=W), 1), (dict(h=WU), 1), (dict(g=X, u=U), 1), (dict(g=G, u=WU), 1),
     (dict(g=G), 1), (dict(u=U), 1), (dict(g=G, u=G), 1), (dict(g=Y, u=U), 1), (dict(g=G, u=P(Y.value + 16)), 1),
     (dict(g=BAD, u=U), 3), (dict(g=G, u=BAD), 3), (dict(bu=BAD), 3), (dict(wu=BAD), 3),
     (dict(M=-1), 1), (dict(N=8), 2), (dict(K=8), 2), (dict(fmt=2, group=32, sg=S, su=SU, K=128), 2),
