@@ -291,21 +291,22 @@ __device__ __forceinline__ RowF row_f(const RowRaw& r, float alpha) {
   return c;
 }
 
-// pre-activation of one element. W8A8: |acc| < 2^31 becomes fp32 with one
-// rounding (2^-24 relative), and the two scales and the bias add three more:
-// 2^-22 in all, a thousandth of the half step of the fp16 result. (The plain
-// W8A8 epilogue is rounded exactly; after an activation there is no exact
-// value to round to.)
+// Pre-activations of two tokens. W8A8: |acc| < 2^31 becomes fp32 with one
+// rounding (2^-24 relative), and the two scales and the bias add two more: less
+// than 2^-22 in all, a thousandth of the half step of the fp16 result. (The
+// plain W8A8 epilogue is rounded exactly; after an activation there is no
+// exact value to round to.)
 template <int KIND>
-__device__ __forceinline__ float pre_act(uint32_t acc, float sx, const RowF& c) {
-  float z;
+__device__ __forceinline__ F2 pre_act2(uint32_t a0, uint32_t a1, float sx0, float sx1, const RowF& c) {
   if constexpr (KIND == kW8A8) {
-    z = __fmul_rn(__fmul_rn(__int2float_rn(static_cast<int32_t>(acc)), sx), c.sw);
+    const F2 t = f2_mul(f2(__int2float_rn(static_cast<int32_t>(a0)), __int2float_rn(static_cast<int32_t>(a1))),
+                        f2(sx0, sx1));
+    return f2_fma(t, f2(c.sw), f2(c.bias));
+  } else if constexpr (KIND == kQ8) {
+    return f2_fma(f2(__uint_as_float(a0), __uint_as_float(a1)), f2(c.sw), f2(c.bias));
   } else {
-    z = __uint_as_float(acc);
-    if constexpr (KIND == kQ8) z = __fmul_rn(z, c.sw);
+    return f2_add(f2(__uint_as_float(a0), __uint_as_float(a1)), f2(c.bias));
   }
-  return __fadd_rn(z, c.bias);
 }
 
 // act(z) + alpha v of two tokens; a zero strength leaves the value's bits alone
@@ -668,9 +669,8 @@ __device__ __forceinline__ void act_chunks(int c_first, int cs, int nchunk, uint
     with_act(p.act, [&](auto tag) {
 #pragma unroll
       for (int i = 0; i < 16; i += 2) {
-        F2 y = act_steer2<decltype(tag)::value>(f2(pre_act<KIND>(r[i], KIND == kW8A8 ? sxv[i] : 0.0f, rc),
-                                                   pre_act<KIND>(r[i + 1], KIND == kW8A8 ? sxv[i + 1] : 0.0f, rc)),
-                                                rc);
+        F2 y = act_steer2<decltype(tag)::value>(
+            pre_act2<KIND>(r[i], r[i + 1], KIND == kW8A8 ? sxv[i] : 0.0f, KIND == kW8A8 ? sxv[i + 1] : 0.0f, rc), rc);
         if (p.res)
           y = f2_add(y, f2(__half2float(box[i * 32 + lane]), __half2float(box[(i + 1) * 32 + lane])));
         const float2 o = f2_get(y);
@@ -745,30 +745,37 @@ __device__ __forceinline__ void gated_chunks_dq(int c_first, int cs, int nchunk,
   tmem_ld16(tacc + c_first * 16, r);
   for (int c = c_first; c < nchunk; c += cs) {
     tmem_ld_wait();
-    float z[16];
+    F2 z[8];  // pairs of tokens
 #pragma unroll
-    for (int i = 0; i < 16; ++i) z[i] = pre_act<KIND>(r[i], 0.0f, rc);
+    for (int i = 0; i < 8; ++i) z[i] = pre_act2<KIND>(r[2 * i], r[2 * i + 1], 0.0f, 0.0f, rc);
     // the next chunk's accumulators travel while this one is computed
     if (c + cs < nchunk) tmem_ld16(tacc + (c + cs) * 16, r);
     else release();
-    float own[8], other[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      own[j] = up ? z[8 + j] : z[j];
-      other[j] = __shfl_xor_sync(0xffffffffu, up ? z[j] : z[8 + j], 16);
-    }
     const int m = m0 + c * 16 + srow;
     const int64_t o = static_cast<int64_t>(m) * p.N + nb + scol;
     const bool in = m < p.M && n_in;
     if (p.G) {  // a training step keeps the pre-activations: a box of either
-      __half* zb = box + 256 + (up ? 256 : 0);
+      __half* zb = box + 256 + (up ? 256 : 0) + ch;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) zb[i * 16 + ch] = __float2half_rn(z[i]);
+      for (int i = 0; i < 8; ++i) {
+        const __half2 h = __float22half2_rn(f2_get(z[i]));
+        zb[(2 * i) * 16] = __low2half(h);
+        zb[(2 * i + 1) * 16] = __high2half(h);
+      }
     }
-    __half h[8];
-    with_act(p.act, [&](auto tag) { gated_out<decltype(tag)::value, 8>(own, other, up, h); });
+    __half* hb = box + (up ? 8 * 16 : 0) + ch;
+    with_act(p.act, [&](auto tag) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) box[((up ? 8 : 0) + j) * 16 + ch] = h[j];
+      for (int j = 0; j < 4; ++j) {
+        const F2 own = up ? z[4 + j] : z[j];
+        const float2 give = f2_get(up ? z[j] : z[4 + j]);
+        const F2 other = f2(__shfl_xor_sync(0xffffffffu, give.x, 16), __shfl_xor_sync(0xffffffffu, give.y, 16));
+        const F2 g = up ? other : own, u = up ? own : other;
+        const __half2 h = __float22half2_rn(f2_get(f2_mul(act_fwd2<decltype(tag)::value>(g), u)));
+        hb[(2 * j) * 16] = __low2half(h);
+        hb[(2 * j + 1) * 16] = __high2half(h);
+      }
+    });
     __syncwarp();
     const uint4 v = reinterpret_cast<const uint4*>(box)[lane];
     if (in) *reinterpret_cast<uint4*>(reinterpret_cast<__half*>(p.Y) + o) = v;
@@ -815,7 +822,12 @@ __device__ __forceinline__ void gated_chunks(int c_first, int cs, int nchunk, ui
     if (c + cs >= nchunk) release();
     float z[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) z[i] = pre_act<KIND>(r[i], KIND == kW8A8 ? sxv[i] : 0.0f, rc);
+    for (int i = 0; i < 16; i += 2) {
+      const float2 f = f2_get(pre_act2<KIND>(r[i], r[i + 1], KIND == kW8A8 ? sxv[i] : 0.0f,
+                                             KIND == kW8A8 ? sxv[i + 1] : 0.0f, rc));
+      z[i] = f.x;
+      z[i + 1] = f.y;
+    }
     // two exchange boxes: a warp writes one again only after the barrier of
     // the chunk in between, which its partner reaches after reading it
     const uint32_t eo = (nst & 1) * kGatedExch;
@@ -911,8 +923,8 @@ __device__ __forceinline__ void split_gated(const uint8_t* red, int n0, int m0, 
     __half h[4], hg[4], hu[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      zg[k] = pre_act<KIND>(g4[k], sxm, rg[k]);
-      zu[k] = pre_act<KIND>(u4[k], sxm, ru[k]);
+      zg[k] = f2_get(pre_act2<KIND>(g4[k], g4[k], sxm, sxm, rg[k])).x;
+      zu[k] = f2_get(pre_act2<KIND>(u4[k], u4[k], sxm, sxm, ru[k])).x;
       hg[k] = __float2half_rn(zg[k]);
       hu[k] = __float2half_rn(zu[k]);
     }
@@ -1729,8 +1741,8 @@ __global__ void __launch_bounds__(KindTraits<KIND>::kThreads, 1)
               with_act(p.act, [&](auto tag) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                  const float z = pre_act<KIND>(a4[k], sxm, rf[k]);
-                  const float y = f2_get(act_steer2<decltype(tag)::value>(f2(z), rf[k])).x;
+                  const F2 z = pre_act2<KIND>(a4[k], a4[k], sxm, sxm, rf[k]);
+                  const float y = f2_get(act_steer2<decltype(tag)::value>(z, rf[k])).x;
                   h[k] = __float2half_rn(p.res ? __fadd_rn(y, __half2float(hr[k])) : y);
                 }
               });
