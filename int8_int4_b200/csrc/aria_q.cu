@@ -156,7 +156,33 @@ aria_status plan_gemm(int kind, int epi, int64_t M, int64_t N, int64_t K, Plan* 
 #if defined(ARIA_MAX_BN)
   dq_policy = false;  // tuning builds pin the tile
 #endif
-  if (dq_policy) {
+  if (dq_policy && epi != kEpiPlain) {
+    // The same choice by estimated time (the rule below is tuned to the plain
+    // linears; two gated projections have twice the tiles, and where they lie
+    // between half and two thirds of the SMs it would halve the token tile
+    // into two waves: q8 6144 x 1536 at M = 203 21.6 against 13.5 us). A K
+    // block takes about 0.21 us and 0.0009 per token of the tile (0.08 more
+    // when the weights go through shared memory), a split-K exchange 1.2 us and
+    // 0.014 per token.
+    const int mt0 = mt;
+    double best = 0.0;
+    int best_mt = mt0;
+    const double nkb = static_cast<double>((K + 63) / 64);
+    for (int m_try = mt0; m_try <= mt0 + 2; ++m_try) {
+      int b = 0;
+      const int m_eff = tile_for(m_try, &b);
+      const int64_t t = static_cast<int64_t>(nt) * m_eff;
+      const int64_t s = t < di.sms ? std::min<int64_t>({8, di.sms / t, p.units}) : 1;
+      const int64_t waves = (t * s + di.sms - 1) / di.sms;
+      const double kb = 0.21 + 0.0009 * b + (t <= di.sms ? 0.0 : 0.08);
+      const double us = waves * (nkb / s * kb + 1.0) + (s > 1 ? 1.2 + 0.014 * b : 0.0) + 0.3 * (m_try - mt0);
+      if (best == 0.0 || us < best) {
+        best = us;
+        best_mt = m_try;
+      }
+    }
+    mt = tile_for(best_mt, &bn);
+  } else if (dq_policy) {
     const int mt0 = mt;
     int best_mt = 0, best_tiles = 0;
     for (int m_try = mt0; m_try <= mt0 + 2; ++m_try) {
