@@ -259,6 +259,31 @@ def test_gated_save_changes_nothing_and_repeats(fmt, M):
     assert not torch.equal(a, aq.qgemm_gated(fmt, X, Wu, su, Wg, sg, sx=sx))
 
 
+@pytest.mark.parametrize("M", [3, 200])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_w8a8_accumulators_at_their_limit(M, sign):
+    """K = 133136, every code at +-127: |acc| = 0.99999 * 2^31, exact in int32;
+    its fp32 image and the scales are off by 2^-24 each, relative."""
+    K, N = 133136, 32
+    assert 2 ** 31 - 2 ** 18 < K * 127 ** 2 < 2 ** 31
+    X = torch.full((M, K), 127, dtype=torch.int8, device="cuda")
+    W = torch.full((N, K), 127 * sign, dtype=torch.int8, device="cuda")
+    sx = torch.rand(M, generator=gen(1)).cuda() + 0.5
+    sw = (torch.rand(N, generator=gen(2)).cuda() + 0.5) * 1e-8
+    z = sx.double()[:, None] * sw.double() * (K * 127 ** 2 * sign)
+    y = aq.qgemm_act("w8a8", X, W, sw, sx=sx, act="silu")
+    close(y, act64(z, "silu"), (H16 + 2.0 ** -18 + 1.13 * 2.0 ** -21) * z.abs() + SUB)
+    h = aq.qgemm_gated("w8a8", X, W, sw, W, sw, sx=sx, act="none")
+    close(h, z * z, (H16 + 2.0 ** -20) * z * z + SUB)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_long_and_narrow(fmt):
+    """Many tiles per CTA: 9001 tokens, one column tile."""
+    check_gated(fmt, 9001, 16, 256, "silu", save=True)
+    check_act(fmt, 9001, 32, 256, "gelu", residual=True, steer=True)
+
+
 # ---------------------------------------------------------------------- backward --
 
 def grads64(dH, G, U, act):
@@ -272,7 +297,7 @@ def bwd_inputs(M, N, K, seed=0):
 
 
 BWD_SIZES = [(1, 16, 16), (2, 128, 64), (7, 208, 144), (64, 64, 64), (100, 272, 400), (129, 1040, 592),
-             (432, 4096, 1024), (1000, 528, 272), (2100, 256, 1040), (4096, 512, 256)]
+             (432, 4096, 1024), (1000, 528, 272), (2100, 256, 1040), (4096, 512, 256), (9001, 32, 48)]
 
 
 @pytest.mark.parametrize("M,N,K", BWD_SIZES)
