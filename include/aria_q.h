@@ -1,6 +1,8 @@
 /*
  * aria_q.h -- C ABI of libaria_q.so: quantized linear layers (q8 / q4
- * weight-only, W8A8) for NVIDIA B200 (sm_100a).
+ * weight-only, W8A8) for NVIDIA B200 (sm_100a), and the feed-forward
+ * operators built on them (activation, residual and gated projections in the
+ * GEMM's epilogue, with the gated block's backward pass).
  *
  * Source of the method: "A Quantized Native Runtime for On-Device Semantic
  * Audio Generation" (aria project page). "What aria is": the diffusion
@@ -39,8 +41,8 @@
  *   - The library allocates no device memory, makes no host-device copies
  *     inside the entry points below, and is safe to call while a stream is
  *     being captured into a CUDA graph (aria_device_status excepted). The
- *     one entry point that needs scratch memory (aria_qgemm_w8a8_fused)
- *     takes it from the caller.
+ *     entry points that need scratch memory (aria_qgemm_w8a8_fused,
+ *     aria_gated_bwd) take it from the caller.
  */
 #ifndef ARIA_Q_H
 #define ARIA_Q_H

@@ -13,6 +13,10 @@ real" (a direction added at one block, bit-identical at alpha = 0), "Live
 steering while streaming" (the strength lives inside the captured graph) and
 "Run it" (the steer spec site:block:file:alpha:steps). Formats and argument
 rules are documented in include/aria_q.h.
+
+qgemm_act, qgemm_gated and gated_backward are the feed-forward operators on
+the same formats: activation, steering and residual in the GEMM's epilogue, a
+gated block's two projections in one kernel, and its gradients.
 """
 from __future__ import annotations
 
@@ -598,14 +602,35 @@ def gated_backward(dH: torch.Tensor, X, Wg, Wu, G: torch.Tensor, U: torch.Tensor
         _arg(workspace, "workspace", workspace.shape, _U8, di)
         if workspace.numel() < need:
             raise ValueError(f"workspace of {workspace.numel()} bytes, {need} needed")
-    lib = load_library()
     raw = _here(di, stream)
-    with contextlib.nullcontext(raw) if raw is not None else _running_on(di, stream) as raw:
-        if out is None:
-            out = tuple([dH.new_empty(sh) if on else None for on, sh in zip(asked, shapes)])
-        ws = workspace if workspace is not None else dH.new_empty(need, dtype=_U8)
-        _check(lib.aria_gated_bwd(a, M, N, K, *pin, *[None if t is None else t.data_ptr() for t in out],
-                                  ws.data_ptr(), ws.numel(), raw))
+    if raw is not None:
+        return _gated_backward_on(raw, a, M, N, K, pin, dH, X, Wg, Wu, input_grad, weight_grad, bias_grad, out,
+                                  workspace, need)
+    with _running_on(di, stream) as raw:
+        return _gated_backward_on(raw, a, M, N, K, pin, dH, X, Wg, Wu, input_grad, weight_grad, bias_grad, out,
+                                  workspace, need)
+
+
+def _gated_backward_on(raw, act, M, N, K, pin, dH, X, Wg, Wu, input_grad, weight_grad, bias_grad, out, ws, need):
+    """The checked call on stream `raw`, with what is not given allocated (the
+    inputs are contiguous, so the tensors like them are)."""
+    if out is None:
+        dX = dWg = dWu = dbg = dbu = None
+        if input_grad:
+            dX = dH.new_empty((M, K)) if X is None else torch.empty_like(X)
+        if weight_grad:
+            dWg = dH.new_empty((N, K)) if Wg is None else torch.empty_like(Wg)
+            dWu = torch.empty_like(dWg)
+        if bias_grad:
+            dbg = dH.new_empty(N)
+            dbu = torch.empty_like(dbg)
+        out = (dX, dWg, dWu, dbg, dbu)
+    if ws is None:
+        ws = dH.new_empty(need, dtype=_U8)
+    st = load_library().aria_gated_bwd(act, M, N, K, *pin, *[None if t is None else t.data_ptr() for t in out],
+                                       ws.data_ptr(), ws.numel(), raw)
+    if st:
+        _check(st)
     return tuple(out)
 
 

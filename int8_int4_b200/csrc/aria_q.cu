@@ -1159,8 +1159,9 @@ aria_status out_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols
 // of the channel-major kernel 2 (128 + BN); a tile's epilogue overlaps the
 // next tile's mainloop in part, and the last one stands alone. The five
 // remaining constants are fitted to a sweep over five weight shapes and nine
-// token counts from 48 to 4096, where the choice for the gated operator then
-// costs 0.6 % over the best of the four variants on average.
+// token counts from 48 to 4096 (180 cases of either operator, the linear with
+// a residual), where the choice then costs 0.6 % over the best of the four
+// variants on average.
 struct TgChoice {
   int bn = 256;
   double us = 0.0;
@@ -1173,7 +1174,7 @@ TgChoice choose_tg(bool gated, int64_t M, int64_t N, int64_t nkb) {
     const int chans = gated ? bn / 2 : bn;
     const int64_t waves = (tr * ((N + chans - 1) / chans) + pairs - 1) / pairs;
     const double kb = std::max(2 * bn, 256 + bn) / 1850.0;  // us per K block
-    const double epi = bn / 64 * (gated ? 0.45 : 1.5);      // a tile's epilogue
+    const double epi = bn / 64 * (gated ? 0.45 : 1.0);      // a tile's epilogue
     const double main = static_cast<double>(nkb) * kb;
     const double t = 2.8 + epi + static_cast<double>(waves) * (1.5 + std::max(main, epi) + 0.75 * std::min(main, epi));
     if (best.us == 0.0 || t < best.us) best = TgChoice{bn, t};
@@ -1184,18 +1185,16 @@ TgChoice choose_tg(bool gated, int64_t M, int64_t N, int64_t nkb) {
 // Measured: gated fp16 over N = 6144, K = 1536 takes 12.8 us against 21.1 at
 // M = 203 and 110 against 163 at M = 4096, but over N = 1536, K = 6144 (few
 // tiles, which only the channel-major kernel splits along K) 28 against 24 at
-// M = 432; a linear with residual wins only where its products outweigh the
-// epilogue: W8A8 at M = 4096, N = 1536, K = 6144 33 against 39 us, at K = 1536
-// 18.4 against 17.6.
+// M = 432; a linear with residual, W8A8 at M = 4096, N = 1536, K = 6144 33
+// against 39, at K = 1536 18.4 against 17.6.
 bool use_tg(int kind, bool gated, int64_t M, int64_t N, int64_t K, int* bn) {
   using namespace aria;
   if ((kind != kF16 && kind != kW8A8) || M < 128 || M > (1 << 30)) return false;  // (row indices: 32 bits)
   const int64_t nkb = (K * (kind == kF16 ? 2 : 1) + 127) / 128;
   const TgChoice tg = choose_tg(gated, M, N, nkb);
   *bn = tg.bn;
-  if (!gated) return 2.0 * static_cast<double>(M) * N * K >= 3e10;
   Plan pl;
-  if (plan_gemm(kind, kEpiGated, M, N, K, &pl) != ARIA_OK) return false;
+  if (plan_gemm(kind, gated ? kEpiGated : kEpiAct, M, N, K, &pl) != ARIA_OK) return false;
   const int64_t sms = dev_info().sms, ctas = static_cast<int64_t>(pl.p.tiles) * pl.p.splits;
   const double kb = 2.0 * (128 + pl.p.BN) / 1850.0, epi = pl.p.BN * 0.022;
   const double main = static_cast<double>(nkb) / pl.p.splits * kb;
