@@ -58,7 +58,7 @@ constexpr int kTgThreads = 128 + 32 * kTgEpiWarps;
 constexpr int kTgEpiStep = kTgEpiWarps / 4;  // warps per TMEM lane quarter: they share a tile's column units
 constexpr int kTgRows = 128;              // rows per CTA; a pair's tile has twice as many
 constexpr uint32_t kTgATile = 16384;      // 128 rows x 64 fp16 (or 128 int8) of k
-constexpr uint32_t kTgAccCols = 256;
+constexpr uint32_t kTgAccCols = 256;      // = the epilogue's threads, which load a tile's column constants
 constexpr uint32_t kTgBox = 32 * 64;      // output box of a warp: 32 rows x 32 fp16
 constexpr int kTgSlots = 3;               // boxes per epilogue warp (two together hold 32 x 32 fp32)
 constexpr uint32_t kTgStageBytes = kTgEpiWarps * kTgSlots * kTgBox;
@@ -518,8 +518,7 @@ __global__ void __launch_bounds__(kTgThreads, 1)
       float* cb = col + b * 3 * kTgAccCols;
       if constexpr (MODE != kTgGrad) {
 #pragma unroll
-        for (int k = 0; k < 3; ++k)
-          if (te < static_cast<int>(kTgAccCols)) cb[k * kTgAccCols + te] = cv[k];
+        for (int k = 0; k < 3; ++k) cb[k * kTgAccCols + te] = cv[k];
         named_bar(1, kTgEpiWarps * 32);  // and every reader of this buffer two items ago is done
         col_load(valid, nx, cv);
       }
