@@ -1077,26 +1077,29 @@ struct TgPlan {
 };
 
 // Ring and shared-memory layout for tiles of 256 rows x `bn` accumulator
-// columns. `bmn`: B is MN-major (boxes of 64 columns).
-aria_status plan_tg(bool bmn, int bn, TgPlan* out) {
+// columns (a gradient's B is MN-major: boxes of 64 columns).
+aria_status plan_tg(int mode, int bn, TgPlan* out) {
   using namespace aria;
   const DevInfo di = dev_info();
   std::memset(&out->p, 0, sizeof(out->p));
   std::memset(&out->m, 0, sizeof(out->m));
   TgParams& p = out->p;
   p.BN = bn;
-  p.b_stage = static_cast<uint32_t>(bmn ? (bn / 2 + 63) / 64 * 64 : bn / 2) * 128u;
-  const int64_t col_bytes = 2 * 3 * kTgAccCols * 4;
-  const int64_t budget = static_cast<int64_t>(di.smem_optin) - 1024 - 512 - col_bytes - kTgStageBytes;
-  const int ns = static_cast<int>(std::min<int64_t>(8, budget / (kTgATile + p.b_stage)));
+  const bool grad = mode == kTgGrad;
+  const uint32_t a_stage = tg_kb_per_stage(mode) * kTgATile;
+  p.b_stage = static_cast<uint32_t>(tg_kb_per_stage(mode) * (grad ? (bn / 2 + 63) / 64 * 64 : bn / 2)) * 128u;
+  const uint32_t col_bytes = grad ? 0 : 2 * 3 * kTgAccCols * 4;
+  const uint32_t out_bytes = kTgEpiWarps * tg_slots(mode) * kTgBox;
+  const int64_t budget = static_cast<int64_t>(di.smem_optin) - 1024 - 512 - col_bytes - out_bytes;
+  const int ns = static_cast<int>(std::min<int64_t>(8, budget / (a_stage + p.b_stage)));
   if (ns < 2) return fail(ARIA_ERR_UNSUPPORTED, "tile does not fit in shared memory");
   p.nstage = ns;
   p.off_a = 0;
-  p.off_b = static_cast<uint32_t>(ns) * kTgATile;
+  p.off_b = static_cast<uint32_t>(ns) * a_stage;
   p.off_out = p.off_b + static_cast<uint32_t>(ns) * p.b_stage;
-  p.off_col = p.off_out + kTgStageBytes;
-  p.off_bar = p.off_col + static_cast<uint32_t>(col_bytes);
-  out->smem = 1024 + p.off_bar + (2 * ns + 5 + kTgEpiWarps * kTgSlots) * 8 + 16;
+  p.off_col = p.off_out + out_bytes;
+  p.off_bar = p.off_col + col_bytes;
+  out->smem = 1024 + p.off_bar + (2 * ns + 5 + kTgEpiWarps * tg_slots(mode)) * 8 + 16;
   if (out->smem > static_cast<size_t>(di.smem_optin))
     return fail(ARIA_ERR_UNSUPPORTED, "shared memory plan too large");
   return ARIA_OK;
@@ -1211,7 +1214,7 @@ aria_status forward_tg(int kind, int bn, int64_t M, int64_t N, int64_t K, const 
   const bool i8 = kind == kW8A8;
   TgPlan pl;
   const int kelems = i8 ? 128 : 64;
-  aria_status s = plan_tg(false, bn, &pl);
+  aria_status s = plan_tg(MODE, bn, &pl);
   if (s != ARIA_OK) return s;
   TgParams& p = pl.p;
   const int chans = MODE == kTgGated ? p.BN / 2 : p.BN;
@@ -1254,9 +1257,9 @@ aria_status forward_tg(int kind, int bn, int64_t M, int64_t N, int64_t K, const 
 // from a 256-byte boundary.
 constexpr int kBwdBn = 256;        // columns of a gradient tile
 constexpr int kBwdMaxParts = 16;
-constexpr int kBwdItemMin = 9;     // K blocks' time that an item's epilogue takes: no item costs less
+constexpr int kBwdItemMin = 5;     // ring stages' time that an item's epilogue takes: no item costs less
 
-// The longest time of a unit, in K blocks, when `units` pairs take n0 items of
+// The longest time of a unit, in ring stages (128 of k), when `units` pairs take n0 items of
 // length l0 first and then n1 <= l0 long ones; the caps go to *sc.
 int64_t bwd_makespan(int units, int64_t n0, int64_t l0, int64_t n1, int64_t l1, aria::TgSched* sc) {
   sc->q = static_cast<int>(n0 / units);
@@ -1295,12 +1298,12 @@ BwdPlan make_bwd_plan(int64_t M, int64_t N, int64_t K, bool dx, bool dw, int uni
   auto tiles = [](int64_t rows, int64_t cols) {
     return (rows + 2 * kTgRows - 1) / (2 * kTgRows) * ((cols + kBwdBn - 1) / kBwdBn);
   };
-  const int64_t tx = dx ? tiles(M, K) : 0, lx = 2 * ((N + 63) / 64);
-  const int64_t tw = dw ? 2 * tiles(N, K) : 0, lw = std::max<int64_t>(kBwdItemMin, (M + 63) / 64);
-  // Shares of k for dX: each more than one costs a further launch that reads
-  // the fp32 partials back, about 10 K blocks' time, and every partial is
-  // written and read once more (a K block moves 64 KB per pair in 0.3 us;
-  // all pairs together write and read partials at about 4 TB/s)
+  const int64_t tx = dx ? tiles(M, K) : 0, lx = 2 * ((N + 127) / 128);
+  const int64_t tw = dw ? 2 * tiles(N, K) : 0, lw = std::max<int64_t>(kBwdItemMin, (M + 127) / 128);
+  // Shares of k for dX: more than one costs a further launch that reads the
+  // fp32 partials back, about 5 stages' time, and every partial is written and
+  // read once more (a stage takes about 0.6 us; all pairs together write and
+  // read partials at about 4 TB/s)
   int64_t best = -1;
   for (int s = 1; s <= kBwdMaxParts && s <= lx; ++s) {
     if (s > 1 && (!dx || tx * s > 4 * units)) break;
@@ -1314,7 +1317,7 @@ BwdPlan make_bwd_plan(int64_t M, int64_t N, int64_t K, bool dx, bool dw, int uni
       t = bwd_makespan(units, tw, lw, tx * s, l, &sc);
       sc.first = 1;
     }
-    if (s > 1) t += 10 + s * (M * K * 8 / 4000) / 300;
+    if (s > 1) t += 5 + s * (M * K * 8 / 4000) / 600;
     if (best < 0 || t < best) {
       best = t;
       sc.n[0] = static_cast<int>(tx * s);
@@ -1512,7 +1515,7 @@ ARIA_API aria_status aria_gated_bwd(aria_act act, int64_t M, int64_t N, int64_t 
   // everything that can be refused comes before the first launch
   TgPlan pl;
   if (dX || dWg) {
-    if ((s = plan_tg(true, kBwdBn, &pl)) != ARIA_OK) return s;
+    if ((s = plan_tg(kTgGrad, kBwdBn, &pl)) != ARIA_OK) return s;
     pl.p.sched = bp.sched;
     pl.p.nunit = bp.units;
     pl.p.M = static_cast<int>(M);
@@ -1524,16 +1527,16 @@ ARIA_API aria_status aria_gated_bwd(aria_act act, int64_t M, int64_t N, int64_t 
     if (dX) {
       if ((s = half_map(&pl.m.A[0], dG, M, N, kTgRows)) != ARIA_OK) return s;
       if ((s = half_map(&pl.m.A[1], dU, M, N, kTgRows)) != ARIA_OK) return s;
-      if ((s = half_map(&pl.m.B[0], Wg, N, K, 64)) != ARIA_OK) return s;
-      if ((s = half_map(&pl.m.B[1], Wu, N, K, 64)) != ARIA_OK) return s;
+      if ((s = half_map(&pl.m.B[0], Wg, N, K, 128)) != ARIA_OK) return s;
+      if ((s = half_map(&pl.m.B[1], Wu, N, K, 128)) != ARIA_OK) return s;
       if ((s = bp.parts > 1 ? partial_map(&pl.m.D[0], xpart, bp.parts, M, K) : out_map(&pl.m.D[0], dX, M, K)) !=
           ARIA_OK)
         return s;
     }
     if (dWg) {
-      if ((s = half_map(&pl.m.A[2], dG, M, N, 64)) != ARIA_OK) return s;
-      if ((s = half_map(&pl.m.A[3], dU, M, N, 64)) != ARIA_OK) return s;
-      if ((s = half_map(&pl.m.B[2], X, M, K, 64)) != ARIA_OK) return s;
+      if ((s = half_map(&pl.m.A[2], dG, M, N, 128)) != ARIA_OK) return s;
+      if ((s = half_map(&pl.m.A[3], dU, M, N, 128)) != ARIA_OK) return s;
+      if ((s = half_map(&pl.m.B[2], X, M, K, 128)) != ARIA_OK) return s;
       if ((s = out_map(&pl.m.D[1], dWg, N, K)) != ARIA_OK) return s;
       if ((s = out_map(&pl.m.D[2], dWu, N, K)) != ARIA_OK) return s;
     }

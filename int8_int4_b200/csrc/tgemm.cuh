@@ -60,8 +60,14 @@ constexpr int kTgRows = 128;              // rows per CTA; a pair's tile has twi
 constexpr uint32_t kTgATile = 16384;      // 128 rows x 64 fp16 (or 128 int8) of k
 constexpr uint32_t kTgAccCols = 256;      // = the epilogue's threads, which load a tile's column constants
 constexpr uint32_t kTgBox = 32 * 64;      // output box of a warp: 32 rows x 32 fp16
-constexpr int kTgSlots = 3;               // boxes per epilogue warp (two together hold 32 x 32 fp32)
-constexpr uint32_t kTgStageBytes = kTgEpiWarps * kTgSlots * kTgBox;
+// Boxes per epilogue warp (two together hold 32 x 32 fp32), and K blocks per
+// ring stage. A box of an MN-major operand is 64 rows wide, so a K block of a
+// gradient takes three or four TMA copies where a forward one takes two, and
+// each further copy costs about 40 ns; two K blocks per stage bring it back
+// to two of 16 KB each (backward at M, N, K = 4096, 6144, 1536: 254 against
+// 288 us).
+__host__ __device__ constexpr int tg_slots(int mode) { return mode == kTgGrad ? 2 : 3; }
+__host__ __device__ constexpr int tg_kb_per_stage(int mode) { return mode == kTgGrad ? 2 : 1; }
 
 struct TgMaps {
   CUtensorMap A[4];  // forward: X; gradients: dG, dU as rows of tokens, then as rows of channels
@@ -93,11 +99,11 @@ struct TgSched {
 
 struct TgParams {
   int R, C;                // forward: output rows and columns
-  int nkb;                 // forward: K blocks (128 bytes of k)
+  int nkb;                 // forward: K blocks (128 bytes of k), one per stage
   int BN;                  // accumulator columns per tile (gated: 2 x channels)
   int tiles_r, tiles, nunit;
   int nstage;
-  uint32_t b_stage;        // bytes of this CTA's part of a B tile
+  uint32_t b_stage;        // bytes of this CTA's part of B in a stage
   uint32_t off_a, off_b, off_out, off_col, off_bar;
   // gradients
   TgSched sched;
@@ -116,12 +122,12 @@ struct TgParams {
 };
 
 // MN-major operand in the 128-byte swizzle layout: boxes of 64 row indexes
-// (128 bytes) x 64 k; 8 k apart = 1024 bytes (SBO), the next 64 row indexes
-// 8 KB further (LBO).
+// (128 bytes) x 128 k; 8 k apart = 1024 bytes (SBO), the next 64 row indexes
+// 16 KB further (LBO).
 __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t smem_addr) {
   uint64_t d = 0;
   d |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFF);
-  d |= static_cast<uint64_t>(8192 >> 4) << 16;   // LBO
+  d |= static_cast<uint64_t>(16384 >> 4) << 16;  // LBO
   d |= static_cast<uint64_t>(1024 >> 4) << 32;   // SBO
   d |= static_cast<uint64_t>(1) << 46;
   d |= static_cast<uint64_t>(2) << 61;
@@ -233,7 +239,7 @@ struct TgItem {
   int type;        // gradients: 0 = dX, 1 = dW
   int src;         // dW: 0 = gate, 1 = up; dX: the share of k
   int r0, c0;      // this CTA's first row; the tile's first column
-  int kb0, kb1;    // K blocks
+  int kb0, kb1;    // ring stages of k
 };
 
 template <int MODE, bool I8>
@@ -244,6 +250,8 @@ __global__ void __launch_bounds__(kTgThreads, 1)
   uint8_t* smem = dyn_smem + (((base_u32 + 1023u) & ~1023u) - base_u32);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kKElems = I8 ? 128 : 64;  // k per 128-byte block
+  constexpr int kKbs = tg_kb_per_stage(MODE), kSlots = tg_slots(MODE);
+  constexpr uint32_t kAStage = kKbs * kTgATile;
 
   const int crank = static_cast<int>(cluster_ctarank());  // place in the pair
   const int unit = static_cast<int>(blockIdx.x) >> 1;
@@ -257,8 +265,8 @@ __global__ void __launch_bounds__(kTgThreads, 1)
   uint64_t* acc_full = empty + p.nstage;   // [2]
   uint64_t* acc_empty = acc_full + 2;      // [2], the pair's first CTA's
   uint64_t* drain = acc_empty + 2;
-  uint64_t* res_full = drain + 1;          // kTgAct: [kTgEpiWarps][kTgSlots]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(res_full + kTgEpiWarps * kTgSlots);
+  uint64_t* res_full = drain + 1;          // kTgAct: [kTgEpiWarps][slots]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(res_full + kTgEpiWarps * kSlots);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   if (threadIdx.x == 0) {
@@ -271,7 +279,7 @@ __global__ void __launch_bounds__(kTgThreads, 1)
       mbar_init(acc_empty + i, 2 * kTgEpiWarps);
     }
     mbar_init(drain, 1);
-    for (int i = 0; i < kTgEpiWarps * kTgSlots; ++i) mbar_init(res_full + i, 1);
+    for (int i = 0; i < kTgEpiWarps * kSlots; ++i) mbar_init(res_full + i, 1);
     *abort_flag = 0;
     fence_mbar_init();
     if constexpr (MODE != kTgGrad) {  // (a gradient launch fills only the maps that it uses)
@@ -317,7 +325,7 @@ __global__ void __launch_bounds__(kTgThreads, 1)
       if (idx >= sc.n[it.type]) return false;
       const int tiles_c = (p.K + p.BN - 1) / p.BN;
       if (it.type == 0) {
-        const int kb_all = 2 * ((p.N + 63) / 64);
+        const int kb_all = 2 * ((p.N + 127) / 128);
         const int tile = idx / p.parts;
         it.src = idx - tile * p.parts;
         it.kb0 = static_cast<int>(static_cast<int64_t>(kb_all) * it.src / p.parts);
@@ -329,7 +337,7 @@ __global__ void __launch_bounds__(kTgThreads, 1)
         it.src = idx >= per;
         const int tile = idx - it.src * per;
         it.kb0 = 0;
-        it.kb1 = (p.M + 63) / 64;
+        it.kb1 = (p.M + 127) / 128;
         it.r0 = (tile / tiles_c) * (2 * kTgRows);
         it.c0 = (tile % tiles_c) * p.BN;
       }
@@ -350,7 +358,7 @@ __global__ void __launch_bounds__(kTgThreads, 1)
   if (warp == 0) {
     // ------------------------------------------------------ TMA producer
     const uint32_t full0 = mapa_shared(smem_u32(full), 0);
-    const uint32_t tx = 2 * (kTgATile + p.b_stage);  // both CTAs' bytes
+    const uint32_t tx = 2 * (kAStage + p.b_stage);   // both CTAs' bytes
     const int bn_cta = p.BN / 2;                     // this CTA's columns of B
     int s = 0;
     uint32_t ph = 0;
@@ -362,24 +370,25 @@ __global__ void __launch_bounds__(kTgThreads, 1)
         if (lane == 0) {
           if (crank == 0) mbar_arrive_expect_tx(full + s, tx);
           const uint32_t bar = full0 + static_cast<uint32_t>(s) * 8u;
-          uint8_t* a = abuf + s * kTgATile;
+          uint8_t* a = abuf + s * kAStage;
           uint8_t* b = bbuf + s * p.b_stage;
           if constexpr (MODE == kTgGrad) {
             const CUtensorMap* mb;
             int x;
             if (it.type == 0) {
-              const int nkb = (p.N + 63) / 64, src = kb >= nkb;
-              x = (kb - src * nkb) * 64;
+              const int nst = (p.N + 127) / 128, src = kb >= nst;
+              x = (kb - src * nst) * 128;
               tg_load(&tm.A[src], bar, a, x, it.r0);
+              tg_load(&tm.A[src], bar, a + kTgATile, x + 64, it.r0);
               mb = &tm.B[src];
             } else {
-              x = kb * 64;
+              x = kb * 128;
               tg_load(&tm.A[2 + it.src], bar, a, it.r0, x);
-              tg_load(&tm.A[2 + it.src], bar, a + 8192, it.r0 + 64, x);
+              tg_load(&tm.A[2 + it.src], bar, a + kTgATile, it.r0 + 64, x);
               mb = &tm.B[2];
             }
             const int c = it.c0 + crank * bn_cta;
-            for (int j = 0; j < bn_cta; j += 64) tg_load(mb, bar, b + j * 128, c + j, x);
+            for (int j = 0; j < bn_cta; j += 64) tg_load(mb, bar, b + j * 256, c + j, x);
           } else {
             const int x = kb * kKElems;
             tg_load(&tm.A[0], bar, a, x, it.r0);
@@ -412,16 +421,27 @@ __global__ void __launch_bounds__(kTgThreads, 1)
         const bool amn = MODE == kTgGrad && it.type == 1;
         constexpr bool bmn = MODE == kTgGrad;
         const uint32_t idesc = idesc0 | (amn ? 1u << 15 : 0u) | (bmn ? 1u << 16 : 0u);
-        const uint32_t astep = amn ? 128 : 2;  // K-major: 32 bytes per 16 k; MN-major: 16 rows of 128 bytes
+        // 16 k further, in descriptor units of 16 bytes: 32 bytes of a K-major
+        // row, or 16 rows of 128 bytes; the second K block of a stage lies
+        // kTgATile further (K-major), or 64 such rows
+        const uint32_t astep = amn ? 128 : 2, ablock = amn ? 512 : kTgATile / 16;
+        const int klim = MODE != kTgGrad ? 0 : it.type == 0 ? p.N : p.M;
+        const int kper = MODE != kTgGrad || it.type == 1 ? 1 << 30 : (p.N + 127) / 128;  // stages per source
         for (int kb = it.kb0; kb < it.kb1; ++kb) {
           if (!(ok = mbar_wait_warp(full + s, ph, abort_flag, 42))) break;
           tc_fence_after();
-          const uint32_t a_u = smem_u32(abuf + s * kTgATile), b_u = smem_u32(bbuf + s * p.b_stage);
+          const uint32_t a_u = smem_u32(abuf + s * kAStage), b_u = smem_u32(bbuf + s * p.b_stage);
           const uint64_t ad = amn ? sdesc_mn_sw128(a_u) : sdesc_sw128(a_u);
           const uint64_t bd = bmn ? sdesc_mn_sw128(b_u) : sdesc_sw128(b_u);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            tg_mma<I8>(dt, ad + astep * j, bd + (bmn ? 128 : 2) * j, idesc, (kb > it.kb0) | (j > 0));
+          for (int h = 0; h < kKbs; ++h) {
+            // a second K block wholly beyond the sum's end holds zeros
+            if (h == 1 && (kb >= kper ? kb - kper : kb) * 128 + 64 >= klim) break;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              tg_mma<I8>(dt, ad + ablock * h + astep * j, bd + (bmn ? 512 * h + 128 * j : 2 * j), idesc,
+                         (kb > it.kb0) | (h > 0) | (j > 0));
+          }
           tg_commit(empty + s);
           if (++s == p.nstage) { s = 0; ph ^= 1u; }
         }
@@ -473,7 +493,7 @@ __global__ void __launch_bounds__(kTgThreads, 1)
       if constexpr (I8) cv[1] = ld_dep_f32((up ? p.sw[1] : p.sw[0]) + c);
       if (MODE == kTgAct && alpha != 0.0f) cv[2] = alpha * ld_dep_f32(p.steer + c);
     };
-    uint8_t* boxes = smem + p.off_out + e * (kTgSlots * kTgBox);
+    uint8_t* boxes = smem + p.off_out + e * (kSlots * kTgBox);
     float cv[3];
     TgItem it, nx;
     bool valid = item_at(0, nx);
@@ -481,7 +501,7 @@ __global__ void __launch_bounds__(kTgThreads, 1)
     int slot = 0;       // the next unit's box
     uint32_t rph = 0;   // parity of its residual's arrival
     // kTgAct: the residual of a unit is loaded by TMA into the box that will
-    // carry the unit's result, kTgSlots - 1 units ahead and across items (the
+    // carry the unit's result, kSlots - 1 units ahead and across items (the
     // lane reads its row of the box, adds, and writes the sum in its place).
     // Read directly, 16 bytes per row and lane, it took longer: W8A8 with relu
     // at M = 4096, N = 6144, K = 1536 49 against 44 us, the down projection 39
@@ -494,11 +514,11 @@ __global__ void __launch_bounds__(kTgThreads, 1)
       if (!pvalid) return;
       if (lane == 0) {
         bulk_wait_read<1>();  // all but the newest store have read their boxes
-        uint64_t* bar = res_full + e * kTgSlots + pslot;
+        uint64_t* bar = res_full + e * kSlots + pslot;
         mbar_arrive_expect_tx(bar, kTgBox);
         tg_load_local(&tm.R, bar, boxes + pslot * kTgBox, pit.c0 + pc * 32, pit.r0 + (warp & 3) * 32);
       }
-      if (++pslot == kTgSlots) pslot = 0;
+      if (++pslot == kSlots) pslot = 0;
       pc += kTgEpiStep;
       if (pc * 32 >= chans || pit.c0 + pc * 32 >= p.C) {
         pc = cg;
@@ -509,7 +529,7 @@ __global__ void __launch_bounds__(kTgThreads, 1)
     };
     if (MODE == kTgAct && p.res) {
       while (pvalid && pit.c0 + pc * 32 >= p.C) pvalid = item_at(++pi, pit);
-      for (int k = 0; k < kTgSlots - 1; ++k) res_issue();
+      for (int k = 0; k < kSlots - 1; ++k) res_issue();
     }
     for (int i = 0; valid; ++i) {
       it = nx;
@@ -541,9 +561,9 @@ __global__ void __launch_bounds__(kTgThreads, 1)
       }
       auto box_store = [&](const CUtensorMap* m, const F2 (&y)[16], int c0) {
         uint8_t* box = boxes + slot * kTgBox;
-        if (++slot == kTgSlots) slot = 0;
+        if (++slot == kSlots) slot = 0;
         if (MODE != kTgAct || !p.res) {  // (with a residual the box is the warp's since its load was issued)
-          if (lane == 0) bulk_wait_read<kTgSlots - 1>();  // the box's last store has read it
+          if (lane == 0) bulk_wait_read<kSlots - 1>();  // the box's last store has read it
           __syncwarp();
         }
         tg_box_row(box, lane, y);
@@ -595,8 +615,8 @@ __global__ void __launch_bounds__(kTgThreads, 1)
             }
           }
           if (p.res) {
-            mbar_wait(res_full + e * kTgSlots + slot, rph, abort_flag, 45);
-            if (slot == kTgSlots - 1) rph ^= 1u;
+            mbar_wait(res_full + e * kSlots + slot, rph, abort_flag, 45);
+            if (slot == kSlots - 1) rph ^= 1u;
             __syncwarp();
             const uint8_t* box = boxes + slot * kTgBox;
 #pragma unroll
