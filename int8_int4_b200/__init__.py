@@ -452,6 +452,9 @@ def _running_on(di: int, stream):
     """Device and stream of one call: yields the stream's handle. With a stream
     of the caller's, tensors that the call allocates come from that stream's
     pool, so the memory is not still in use by work on another one."""
+    dev = getattr(stream, "device", None)
+    if dev is not None and dev.index != di:
+        raise ValueError(f"the stream belongs to {dev}, the arguments to cuda:{di}")
     with torch.cuda.device(di):
         if stream is None:
             yield torch._C._cuda_getCurrentRawStream(di)
@@ -520,6 +523,8 @@ def qgemm_gated(fmt: str, X: torch.Tensor, Wg: torch.Tensor, scales_g, Wu: torch
     pbu = _arg(bias_u, "bias_u", n, _F16, di)
     if save is None:
         pG = pU = None
+    elif len(save) != 2 or save[0] is None or save[1] is None:
+        raise ValueError("save is (G, U)")
     else:
         pG = _arg(save[0], "save[0]", mn, _F16, di)
         pU = _arg(save[1], "save[1]", mn, _F16, di)

@@ -179,3 +179,20 @@ def test_backward_binding_refusals(lib, kw, err):
     args = dict(dH=meta(4, 32), X=meta(4, 64), Wg=meta(32, 64), Wu=meta(32, 64), G=meta(4, 32), U=meta(4, 32))
     with pytest.raises(err):
         aq.gated_backward(**{**args, **kw})
+
+
+def test_binding_refuses_a_stream_of_another_device(lib):
+    class S:
+        device, cuda_stream = torch.device("cuda:1"), 0
+    with pytest.raises(ValueError, match="cuda:1"):
+        aq.qgemm_act("f16", meta(4, 64), meta(32, 64), None, stream=S())
+    with pytest.raises(ValueError, match="cuda:1"):
+        aq.qgemm_gated("f16", meta(4, 64), meta(32, 64), None, meta(32, 64), None, stream=S())
+    with pytest.raises(ValueError, match="cuda:1"):
+        aq.gated_backward(meta(4, 32), meta(4, 64), meta(32, 64), meta(32, 64), meta(4, 32), meta(4, 32), stream=S())
+
+
+@pytest.mark.parametrize("save", [(), (meta(4, 32),), (meta(4, 32), None), (None, None)])
+def test_gated_keeps_both_or_neither(save):
+    with pytest.raises(ValueError, match="save"):
+        aq.qgemm_gated("f16", meta(4, 64), meta(32, 64), None, meta(32, 64), None, save=save)
