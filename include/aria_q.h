@@ -229,8 +229,9 @@ aria_status aria_qgemm_act(aria_format fmt, int group, int64_t M, int64_t N, int
  *   H, G and U must not overlap one another, X or a weight (INVALID_ARG), nor
  *   any other input.
  * g and u stay in fp32 up to the product; H is rounded once. Shape rules,
- * errors and stream order as for aria_qgemm; both weights are loaded before
- * the dependency wait. Deterministic; H does not depend on whether G and U
+ * errors and stream order as for aria_qgemm, for both weights; a call that
+ * keeps G and U, whose weights an optimiser may just have written, starts
+ * after the preceding kernel, whatever that one is. Deterministic; H does not depend on whether G and U
  * are kept.
  */
 aria_status aria_qgemm_gated(aria_format fmt, int group, int64_t M, int64_t N, int64_t K,

@@ -340,6 +340,14 @@ void set_pdl(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr) {
   cfg.attrs = attr;
 }
 
+// Kernels that load weights before the dependency wait start early only where
+// the pre-activations are not kept: a call that keeps them is a training step's,
+// whose weights the preceding kernel (an optimiser's) may have written by
+// ordinary stores.
+void set_pdl_for_weights(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, const void* kept) {
+  if (!kept) set_pdl(cfg, attr);
+}
+
 // how many clusters of `size` CTAs of this kernel can be resident at once on
 // the current device (cached per device, size and shared-memory footprint;
 // queried outside any capture on first use)
@@ -422,7 +430,7 @@ aria_status launch_gemm(const Plan& pl, const CUtensorMap& tw, const CUtensorMap
     cfg.numAttrs = 1;
     cfg.attrs = attr;
   }
-  set_pdl(cfg, attr);
+  set_pdl_for_weights(cfg, attr, prm.G);
   prm.trace_launch = next_trace_launch();
   cudaError_t e = cudaLaunchKernelEx(&cfg, kfn, tw, ts, tx, prm, tu);
   if (e != cudaSuccess) return cuda_fail(e, "qgemm launch");
@@ -595,7 +603,7 @@ aria_status launch_small_t(const SmallPlan& pl, cudaStream_t st) {
     cfg.numAttrs = 1;
     cfg.attrs = attr;
   }
-  set_pdl(cfg, attr);
+  set_pdl_for_weights(cfg, attr, pl.p.G);
   aria::SmallParams sp = pl.p;
   sp.trace_launch = next_trace_launch();
   cudaError_t e = cudaLaunchKernelEx(&cfg, kfn, sp);

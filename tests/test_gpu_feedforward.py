@@ -462,6 +462,40 @@ def test_training_step_captured_while_an_eager_one_lives(M):
         assert all(torch.equal(a, b) for a, b in zip(out, refs[k]))
 
 
+@pytest.mark.parametrize("M", [1, 16, 64, 100, 300])
+def test_weights_written_by_the_preceding_kernel(M):
+    """A training loop's forward right behind the update of its weights: the
+    call that keeps G and U sees the weights that an ordinary kernel before it
+    in the stream writes, eager and captured."""
+    N, K = 1536, 512
+    X, Wg, Wu = normal(1, M, K), normal(2, N, K, std=0.05), normal(3, N, K, std=0.05)
+    g0, u0 = Wg.clone(), Wu.clone()
+    G, U = (torch.empty(M, N, dtype=torch.float16, device="cuda") for _ in range(2))
+    refs = []
+    for k in (1.0, 0.5, -2.0):  # exact factors
+        torch.cuda.synchronize()
+        H = aq.qgemm_gated("f16", X, g0 * k, None, u0 * k, None, save=(G, U))
+        torch.cuda.synchronize()
+        refs.append((H.clone(), G.clone(), U.clone()))
+
+    def run(i, k):
+        torch.mul(u0, k, out=Wu)
+        torch.mul(g0, k, out=Wg)
+        return aq.qgemm_gated("f16", X, Wg, None, Wu, None, save=(G, U))
+    graph = torch.cuda.CUDAGraph()
+    outs = []
+    with torch.cuda.graph(graph):
+        for i, k in enumerate((1.0, 0.5, -2.0)):
+            outs.append((run(i, k), G.clone(), U.clone()))
+    for _ in range(20):
+        for i, k in enumerate((1.0, 0.5, -2.0)):
+            H = run(i, k)
+            assert all(torch.equal(a, b) for a, b in zip((H, G, U), refs[i]))
+        graph.replay()
+        for i in range(3):
+            assert all(torch.equal(a, b) for a, b in zip(outs[i], refs[i]))
+
+
 def test_two_streams_at_once():
     """Independent calls on two streams, each with its own workspace."""
     M, N, K = 300, 528, 272
