@@ -207,7 +207,9 @@ aria_status aria_qgemm_steer_dev(aria_format fmt, int group, int64_t M, int64_t 
  *   rounded from an fp32 value, like the others (the scales and the bias are
  *   off by at most 2^-22 relative, the activation by less than 2^-16).
  * Deterministic; stream order as for aria_qgemm (the residual is touched only
- * after the preceding kernel).
+ * after the preceding kernel), except that fp16 weights, which any kernel may
+ * have written, are read only after the preceding kernel too: they need no
+ * care. Packed weights keep aria_qgemm's rule.
  */
 aria_status aria_qgemm_act(aria_format fmt, int group, int64_t M, int64_t N, int64_t K,
                            const void *X, const float *sx, const void *Wq, const void *scales,
@@ -229,10 +231,9 @@ aria_status aria_qgemm_act(aria_format fmt, int group, int64_t M, int64_t N, int
  *   H, G and U must not overlap one another, X or a weight (INVALID_ARG), nor
  *   any other input.
  * g and u stay in fp32 up to the product; H is rounded once. Shape rules,
- * errors and stream order as for aria_qgemm, for both weights; a call that
- * keeps G and U, whose weights an optimiser may just have written, starts
- * after the preceding kernel, whatever that one is. Deterministic; H does not depend on whether G and U
- * are kept.
+ * errors and stream order as for aria_qgemm_act, for both weights; a call that
+ * keeps G and U reads its weights only after the preceding kernel in every
+ * format. Deterministic; H does not depend on whether G and U are kept.
  */
 aria_status aria_qgemm_gated(aria_format fmt, int group, int64_t M, int64_t N, int64_t K,
                              const void *X, const float *sx, const void *Wg, const void *scales_g,

@@ -250,7 +250,13 @@ def qgemm(fmt: str, X: torch.Tensor, Wq: torch.Tensor, scales, sx=None,
     fmt "f16" takes the fp16 weight [N,K] as Wq and scales=None. With
     ``alpha_dev`` (one fp32 element on the device, e.g. ``schedule[s:s+1]``)
     the strength is read from device memory when the kernel runs
-    (aria_qgemm_steer_dev) and ``alpha`` is ignored."""
+    (aria_qgemm_steer_dev) and ``alpha`` is ignored.
+
+    The weight and its scales may be read before the preceding kernel in the
+    stream has ended (include/aria_q.h, stream order): qpack-then-qgemm is
+    safe, but where another kernel has just written them (``copy_``, an
+    optimiser's update of an fp16 weight), at least one kernel must lie
+    between; qgemm_act reads fp16 weights in stream order."""
     if fmt != "f16" and scales is None:
         raise ValueError(f"{fmt} needs scales")
     M, N, K = check_gemm_args(fmt, X, Wq, scales, sx, bias, steer_vec, out, alpha_dev)
@@ -473,7 +479,9 @@ def qgemm_act(fmt: str, X: torch.Tensor, Wq: torch.Tensor, scales, sx=None, bias
 
     Formats and arguments as for qgemm; ``act`` is one of ACTS; ``residual``
     fp16 [M,N] may be ``out`` itself. With ``alpha_dev`` the strength is read
-    from device memory and ``alpha`` is ignored."""
+    from device memory and ``alpha`` is ignored. "f16" weights are read in
+    stream order, so they may be written right before the call; packed weights
+    follow qgemm's rule."""
     M, N, K, di, px, psx = _x_args(fmt, X, Wq, sx)
     pw, ps = _weight_args(fmt, Wq, scales, "", N, K, di)
     mn, n = (M, N), (N,)
@@ -514,7 +522,9 @@ def qgemm_gated(fmt: str, X: torch.Tensor, Wg: torch.Tensor, scales_g, Wu: torch
 
     Both weights have one format and shape (as Wq and scales of qgemm; "f16"
     takes the fp16 weights and None for the scales). ``save`` = (G, U): fp16
-    [M,N] tensors that receive g and u, for gated_backward."""
+    [M,N] tensors that receive g and u, for gated_backward. The weights are
+    read in stream order for "f16" and wherever ``save`` is given; packed
+    weights otherwise follow qgemm's rule."""
     M, N, K, di, px, psx = _x_args(fmt, X, Wg, sx)
     pg, psg = _weight_args(fmt, Wg, scales_g, "g", N, K, di)
     pu, psu = _weight_args(fmt, Wu, scales_u, "u", N, K, di)

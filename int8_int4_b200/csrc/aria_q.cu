@@ -331,21 +331,14 @@ int next_trace_launch() { return 0; }
 
 // programmatic dependent launch: the kernel may start while the previous
 // kernel in the stream drains; it waits (griddepcontrol.wait) before reading
-// anything that kernel may write (the GEMM's packed weights are the one
-// exception, see the stream-order note of aria_qgemm in the header)
+// anything that kernel may write (the weights of aria_qgemm and the packed
+// weights of the feed-forward operators are the one exception, see the
+// stream-order note of aria_qgemm in the header)
 void set_pdl(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr) {
   attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
   cfg.numAttrs++;
   cfg.attrs = attr;
-}
-
-// Kernels that load weights before the dependency wait start early only where
-// the pre-activations are not kept: a call that keeps them is a training step's,
-// whose weights the preceding kernel (an optimiser's) may have written by
-// ordinary stores.
-void set_pdl_for_weights(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, const void* kept) {
-  if (!kept) set_pdl(cfg, attr);
 }
 
 // how many clusters of `size` CTAs of this kernel can be resident at once on
@@ -430,7 +423,7 @@ aria_status launch_gemm(const Plan& pl, const CUtensorMap& tw, const CUtensorMap
     cfg.numAttrs = 1;
     cfg.attrs = attr;
   }
-  set_pdl_for_weights(cfg, attr, prm.G);
+  set_pdl(cfg, attr);
   prm.trace_launch = next_trace_launch();
   cudaError_t e = cudaLaunchKernelEx(&cfg, kfn, tw, ts, tx, prm, tu);
   if (e != cudaSuccess) return cuda_fail(e, "qgemm launch");
@@ -603,7 +596,7 @@ aria_status launch_small_t(const SmallPlan& pl, cudaStream_t st) {
     cfg.numAttrs = 1;
     cfg.attrs = attr;
   }
-  set_pdl_for_weights(cfg, attr, pl.p.G);
+  set_pdl(cfg, attr);
   aria::SmallParams sp = pl.p;
   sp.trace_launch = next_trace_launch();
   cudaError_t e = cudaLaunchKernelEx(&cfg, kfn, sp);
@@ -769,7 +762,15 @@ struct EpiArgs {
   const void* bias_u = nullptr;
   void* G = nullptr;             // kEpiGated: the pre-activations
   void* U = nullptr;
+  bool w_late = false;           // no weight load before the dependency wait
 };
+
+// Whether a feed-forward operator's weights may come from the preceding
+// kernel. fp16 weights are ordinary tensors that any kernel may have written
+// by ordinary stores (an optimiser's, a cast, a merge of two weights), and a
+// call that keeps the pre-activations is a training step's in any format.
+// Packed weights otherwise follow aria_qgemm's rule.
+static bool weights_late(int kind, const void* kept) { return kind == aria::kF16 || kept; }
 
 static aria_status check_gemm_sizes(int kind, int64_t M, int64_t N, int64_t K) {
   using namespace aria;
@@ -822,6 +823,7 @@ static aria_status qgemm_impl(int kind, int64_t M, int64_t N, int64_t K, const v
     sp.p.alpha = sp.p.steer ? alpha : 0.0f;
     sp.p.alpha_dev = sp.p.steer ? alpha_dev : nullptr;
     sp.p.Y = static_cast<__half*>(Y);
+    sp.p.w_late = ea.w_late;
     sp.p.act = ea.act;
     sp.p.res = static_cast<const __half*>(ea.res);
     sp.p.W_u = static_cast<const uint8_t*>(ea.Wu);
@@ -869,6 +871,7 @@ static aria_status qgemm_impl(int kind, int64_t M, int64_t N, int64_t K, const v
     pl.p.gbar = ws->gbar;
     pl.p.sx = ws->sx;
   }
+  pl.p.w_late = ea.w_late;
   pl.p.act = ea.act;
   pl.p.res = static_cast<const __half*>(ea.res);
   pl.p.sw_u = static_cast<const float*>((kind == kQ4 || kind == kF16) ? nullptr : ea.scales_u);
@@ -1401,10 +1404,11 @@ ARIA_API aria_status aria_qgemm_act(aria_format fmt, int group, int64_t M, int64
     return fail(ARIA_ERR_INVALID_ARG, "Y overlaps X or the weights");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (!steer_vec) alpha_dev = nullptr;
+  EpiArgs ea;
+  ea.w_late = weights_late(kind, nullptr);
   if (act == ARIA_ACT_NONE && !residual)  // the plain GEMM, byte for byte
     return qgemm_impl<aria::kEpiPlain>(kind, M, N, K, X, sx, Wq, scales, bias, steer_vec, alpha, alpha_dev, Y,
-                                       st, EpiArgs{});
-  EpiArgs ea;
+                                       st, ea);
   ea.act = act;
   ea.res = residual;
   int bn = 0;
@@ -1437,6 +1441,7 @@ ARIA_API aria_status aria_qgemm_gated(aria_format fmt, int group, int64_t M, int
         overlap(Wu, weight_bytes(kind, N, K), o, yb))
       return fail(ARIA_ERR_INVALID_ARG, "an output overlaps X or a weight");
   EpiArgs ea;
+  ea.w_late = weights_late(kind, G);
   ea.act = act;
   ea.Wu = Wu;
   ea.scales_u = scales_u;

@@ -114,6 +114,10 @@ struct GemmParams {
   int helpers;
   int trace_launch;       // trace builds: the launch's index since the trace was cleared
   void* Y;                // fp16 [M,N], or int32 [M,N] for kS32 (split-K path)
+  // the weights may come from the preceding kernel: no weight load before the
+  // dependency wait (the feed-forward operators on fp16 weights, or keeping
+  // their pre-activations)
+  int w_late;
   // kEpiAct, kEpiGated
   int act;
   const __half* res;      // kEpiAct: R [M,N] or null; may be Y itself
@@ -1122,11 +1126,13 @@ __global__ void __launch_bounds__(KindTraits<KIND>::kThreads, 1)
   // the wait: the raw units of the first tile (q8/q4) or the weight half of
   // its first stages (W8A8, whose activation half follows after the wait on
   // the same barrier). Activations, their scales and the output wait for
-  // the preceding kernel to complete.
+  // the preceding kernel to complete, and so do the weights of a launch with
+  // w_late (pre = 0: the ordinary loads behind the wait bring every tile).
   int issued_w = 0, issued_x = 0;  // kept for the teardown drain
   int pre = 0;                     // raw units / stages of the first tile issued before the wait
   if (warp == 0) {
-    if (tile0 < p.tiles) pre = T::kDequant ? (nu < p.n_raw ? nu : p.n_raw) : (nkb < p.n_a ? nkb : p.n_a);
+    const bool late = (KIND == kF16 || EPI != kEpiPlain) && p.w_late;
+    if (tile0 < p.tiles && !late) pre = T::kDequant ? (nu < p.n_raw ? nu : p.n_raw) : (nkb < p.n_a ? nkb : p.n_a);
     uint64_t* pre_full = T::kDequant ? raw_full : st_full;  // arrival count 1 in both rings
     const int nbar = 2 * (p.n_raw + p.n_a) + 6;
     if (lane == 0) {

@@ -62,6 +62,7 @@ struct SmallParams {
   float alpha;
   const float* alpha_dev;
   __half* Y;              // [M,N]
+  int w_late;             // the weights may come from the preceding kernel: loaded behind the dependency wait
   // kEpiAct: activation and residual [M,N] (null: none; may be Y itself)
   int act;
   const __half* res;
@@ -218,7 +219,9 @@ __global__ void __launch_bounds__(kSmThreads, 2) smallm_kernel(const SmallParams
   __syncthreads();
   // ---- all weight bytes of this CTA, before the dependency wait: every
   // thread issues the bulk copies of its share of the rows (one warp issuing
-  // them all serialises the requests)
+  // them all serialises the requests). Weights that the preceding kernel may
+  // have written (w_late) are copied behind the wait instead.
+  if (p.w_late) pdl_wait();
   {
     const uint64_t pol = policy_evict_first();  // streamed once
     for (int r = tid; r < R; r += kSmThreads) {
