@@ -645,6 +645,9 @@ __device__ __forceinline__ void act_chunks(int c_first, int cs, int nchunk, uint
   }
   uint4 rv[2];
   if (p.res) residual_load(c_first, nb, m0, lane, p, rv);
+  // the previous tile's last store may have read the box that this tile starts
+  // with (its chunks are counted anew): no lane writes there before all have
+  __syncwarp();
   int nst = 0;
   for (int c = c_first; c < nchunk; c += cs, ++nst) {
     uint8_t* sbuf = sb0 + (nst & 1) * T::kStageBuf;
