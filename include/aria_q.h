@@ -37,7 +37,10 @@
  *   - Kernels bound every wait. A wait that runs out (about 4 s) records
  *     ARIA_ERR_TIMEOUT in a device status word, and the kernel returns;
  *     aria_device_status() reports and clears it.
- *   - Non-finite inputs are outside the contract (not checked).
+ *   - Non-finite inputs are outside the contract (not checked). The
+ *     activations of the feed-forward operators pass them on as IEEE
+ *     arithmetic does, so that an overflow stays visible: a NaN stays one,
+ *     act(+inf) is +inf, relu(-inf) is 0, the others give NaN at -inf.
  *   - The library allocates no device memory, makes no host-device copies
  *     inside the entry points below, and is safe to call while a stream is
  *     being captured into a CUDA graph (aria_device_status excepted). The

@@ -8,6 +8,10 @@
 // against 64 bits on a million points, |z| <= 8: largest relative error silu
 // 5e-7, gelu 3.3e-6, gelu_tanh 8e-6 (half a step of fp16 is 4.9e-4);
 // derivatives 2e-6 absolute.
+//
+// At infinities and NaN each gives what its formula gives in IEEE arithmetic:
+// a NaN stays one, act(+inf) is +inf, relu(-inf) is 0, and the others, which
+// multiply -inf by 0 there, NaN.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -20,6 +24,13 @@ enum Act : int { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGel
 __device__ __forceinline__ float fast_rcp(float x) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// max(x, 0) that keeps a NaN (fmaxf would return the 0 and hide it)
+__device__ __forceinline__ float relu1(float x) {
+  float r;
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(x));
   return r;
 }
 
@@ -103,6 +114,14 @@ __device__ __forceinline__ F2 normal_tail2(F2 a, F2& gauss) {
   return f2_mul(f2_mul(r, t), gauss);
 }
 
+// z Phi(z) = max(z, 0) - |z| Q(|z|): no cancellation on either side. `m` holds
+// -|z|, for positive z no lower than -64 (Q is 0 far before that): at
+// +infinity, -infinity times 0 would make a NaN of a value that is +infinity.
+__device__ __forceinline__ F2 gelu_of2(float2 v, F2 q) {
+  const F2 m = f2(fminf(v.x, -fminf(v.x, 64.0f)), fminf(v.y, -fminf(v.y, 64.0f)));
+  return f2_fma(m, q, f2(relu1(v.x), relu1(v.y)));
+}
+
 // 1 / (1 + exp(-z)), z scaled by -log2(e) already. exp overflows to infinity
 // below z = -88.7: the reciprocal is then 0, as it should be to fp16.
 __device__ __forceinline__ F2 f2_sigmoid_of(F2 neg_z_log2e) {
@@ -113,15 +132,13 @@ template <int ACT>
 __device__ __forceinline__ F2 act_fwd2(F2 z) {
   if constexpr (ACT == kActRelu) {
     const float2 v = f2_get(z);
-    return f2(fmaxf(v.x, 0.0f), fmaxf(v.y, 0.0f));
+    return f2(relu1(v.x), relu1(v.y));
   } else if constexpr (ACT == kActSilu) {
     return f2_mul(z, f2_sigmoid_of(f2_mul(z, f2(-kLog2e))));
   } else if constexpr (ACT == kActGelu) {
-    // z Phi(z) = max(z, 0) - |z| Q(|z|): no cancellation on either side
     const float2 v = f2_get(z);
-    const F2 a = f2(fabsf(v.x), fabsf(v.y));
     F2 g;
-    return f2_fma(f2_mul(a, f2(-1.0f)), normal_tail2(a, g), f2(fmaxf(v.x, 0.0f), fmaxf(v.y, 0.0f)));
+    return gelu_of2(v, normal_tail2(f2(fabsf(v.x), fabsf(v.y)), g));
   } else if constexpr (ACT == kActGeluTanh) {
     // z (1 + tanh w) / 2 = z sigmoid(2 w), w = sqrt(2/pi) (z + 0.044715 z^3)
     constexpr float k = -2.0f * kTanhC0 * kLog2e;
@@ -143,7 +160,7 @@ __device__ __forceinline__ void act_fwd_bwd2(F2 z, F2& f, F2& d) {
   const F2 one = f2(1.0f), minus = f2(-1.0f);
   if constexpr (ACT == kActRelu) {
     const float2 v = f2_get(z);
-    f = f2(fmaxf(v.x, 0.0f), fmaxf(v.y, 0.0f));
+    f = f2(relu1(v.x), relu1(v.y));
     d = f2(v.x > 0.0f ? 1.0f : 0.0f, v.y > 0.0f ? 1.0f : 0.0f);
   } else if constexpr (ACT == kActSilu) {
     // s + z s (1 - s): 1 - s cancels for large z, where it is a small part of
@@ -154,10 +171,10 @@ __device__ __forceinline__ void act_fwd_bwd2(F2 z, F2& f, F2& d) {
   } else if constexpr (ACT == kActGelu) {
     // Phi(z) + z phi(z), Phi from the upper tail Q(|z|)
     const float2 v = f2_get(z);
-    const F2 a = f2(fabsf(v.x), fabsf(v.y));
     F2 g;
-    const float2 q = f2_get(normal_tail2(a, g));
-    f = f2_fma(f2_mul(a, minus), f2(q.x, q.y), f2(fmaxf(v.x, 0.0f), fmaxf(v.y, 0.0f)));
+    const F2 q2 = normal_tail2(f2(fabsf(v.x), fabsf(v.y)), g);
+    const float2 q = f2_get(q2);
+    f = gelu_of2(v, q2);
     d = f2_fma(f2_mul(z, f2(0.3989422804014327f)), g, f2(v.x > 0.0f ? 1.0f - q.x : q.x, v.y > 0.0f ? 1.0f - q.y : q.y));
   } else if constexpr (ACT == kActGeluTanh) {
     constexpr float c = 2.0f * kTanhC0;
