@@ -558,9 +558,12 @@ def qgemm_gated(fmt: str, X: torch.Tensor, Wg: torch.Tensor, scales_g, Wu: torch
     return out
 
 
-def gated_backward_workspace_size(M: int, N: int, K: int) -> int:
+def gated_backward_workspace_size(M: int, N: int, K: int, device=None) -> int:
+    """Bytes that gated_backward needs on `device` (the current one if None):
+    the number of its SMs decides how dX's sum is divided."""
     n = ctypes.c_size_t()
-    _check(load_library().aria_gated_bwd_workspace_size(M, N, K, ctypes.byref(n)))
+    with contextlib.nullcontext() if device is None else torch.cuda.device(torch.device(device)):
+        _check(load_library().aria_gated_bwd_workspace_size(M, N, K, ctypes.byref(n)))
     return n.value
 
 
@@ -572,8 +575,8 @@ def gated_backward(dH: torch.Tensor, X, Wg, Wu, G: torch.Tensor, U: torch.Tensor
     dbg [N], dbu [N]), fp16, None for those not asked for.
 
     ``out``: a tuple of five tensors to write (None where nothing is asked
-    for). ``workspace``: a uint8 tensor of gated_backward_workspace_size(M, N, K)
-    bytes; calls sharing one must not overlap on the GPU. X is needed for the
+    for). ``workspace``: a uint8 tensor of gated_backward_workspace_size(M, N, K,
+    dH.device) bytes; calls sharing one must not overlap on the GPU. X is needed for the
     weight gradients only and the weights for dX only; K comes from either."""
     if dH.dim() != 2:
         raise ValueError("dH must be 2-D")
@@ -612,23 +615,26 @@ def gated_backward(dH: torch.Tensor, X, Wg, Wu, G: torch.Tensor, U: torch.Tensor
             if (t is not None) != on:
                 raise ValueError(f"out: {n} is {'needed' if on else 'not asked for'}")
             _arg(t, n, sh, _F16, di)
-    need = gated_backward_workspace_size(M, N, K)
     if workspace is not None:
         _arg(workspace, "workspace", workspace.shape, _U8, di)
-        if workspace.numel() < need:
-            raise ValueError(f"workspace of {workspace.numel()} bytes, {need} needed")
+        if workspace.numel() < 4 * M * N:
+            raise ValueError(f"workspace of {workspace.numel()} bytes, more than {4 * M * N} needed")
     raw = _here(di, stream)
     if raw is not None:
         return _gated_backward_on(raw, a, M, N, K, pin, dH, X, Wg, Wu, input_grad, weight_grad, bias_grad, out,
-                                  workspace, need)
+                                  workspace)
     with _running_on(di, stream) as raw:
         return _gated_backward_on(raw, a, M, N, K, pin, dH, X, Wg, Wu, input_grad, weight_grad, bias_grad, out,
-                                  workspace, need)
+                                  workspace)
 
 
-def _gated_backward_on(raw, act, M, N, K, pin, dH, X, Wg, Wu, input_grad, weight_grad, bias_grad, out, ws, need):
+def _gated_backward_on(raw, act, M, N, K, pin, dH, X, Wg, Wu, input_grad, weight_grad, bias_grad, out, ws):
     """The checked call on stream `raw`, with what is not given allocated (the
-    inputs are contiguous, so the tensors like them are)."""
+    inputs are contiguous, so the tensors like them are). The device of the
+    tensors is current: the workspace is planned for it."""
+    need = gated_backward_workspace_size(M, N, K)
+    if ws is not None and ws.numel() < need:
+        raise ValueError(f"workspace of {ws.numel()} bytes, {need} needed")
     if out is None:
         dX = dWg = dWu = dbg = dbu = None
         if input_grad:
