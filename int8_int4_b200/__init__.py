@@ -586,7 +586,7 @@ def gated_backward(dH: torch.Tensor, X, Wg, Wu, G: torch.Tensor, U: torch.Tensor
     if not (input_grad or weight_grad or bias_grad):
         raise ValueError("no gradient is asked for")
     M, N = dH.shape
-    src = X if X is not None else Wg
+    src = X if X is not None else Wg if Wg is not None else Wu
     if src is None:
         if input_grad or weight_grad:
             raise ValueError("dX needs Wg and Wu, dWg and dWu need X")

@@ -86,3 +86,13 @@ def test_workspace_size_of_a_device(monkeypatch):
     for d in (1, "cuda:1", torch.device("cuda:1")):
         assert aq.gated_backward_workspace_size(M, N, K, device=d) == 4 * M * N + 2000
     assert aq.gated_backward_workspace_size(M, N, K) == 4 * M * N + 1000
+
+
+@pytest.mark.parametrize("given", ["X", "Wg", "Wu"])
+def test_bias_gradients_accept_any_of_the_inputs(monkeypatch, given):
+    """K comes from whichever of X and the weights is given; none is needed."""
+    lib = Lib(monkeypatch)
+    only = dict(X=None, Wg=None, Wu=None, input_grad=False, weight_grad=False, out=(None,) * 3 + (fake(N), fake(N)))
+    backward(0, 4 * M * N + 1000, **only)
+    backward(0, 4 * M * N + 1000, **{**only, given: fake(*((M, K) if given == "X" else (N, K)))})
+    assert [c[2] for c in lib.calls if c[0] == "bwd"] == [16, K]
