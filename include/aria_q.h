@@ -207,8 +207,9 @@ aria_status aria_qgemm_steer_dev(aria_format fmt, int group, int64_t M, int64_t 
  *   Every other argument and rule as for aria_qgemm. The epilogue is computed
  *   in fp32 and rounded once, for W8A8 too: with act = NONE and no residual
  *   the call is aria_qgemm, byte for byte; otherwise W8A8 results are
- *   rounded from an fp32 value, like the others (the scales and the bias are
- *   off by at most 2^-22 relative, the activation by less than 2^-16).
+ *   rounded from an fp32 value, like the others: the pre-activation is off by
+ *   at most 2^-22 (|main| + |bias|), which is far below the fp16 step unless
+ *   the two nearly cancel, the activation by less than 2^-16 relative.
  * Deterministic; stream order as for aria_qgemm (the residual is touched only
  * after the preceding kernel), except that fp16 weights, which any kernel may
  * have written, are read only after the preceding kernel too: they need no

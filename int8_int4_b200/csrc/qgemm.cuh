@@ -296,10 +296,11 @@ __device__ __forceinline__ RowF row_f(const RowRaw& r, float alpha) {
 }
 
 // Pre-activations of two tokens. W8A8: |acc| < 2^31 becomes fp32 with one
-// rounding (2^-24 relative), and the two scales and the bias add two more: less
-// than 2^-22 in all, a thousandth of the half step of the fp16 result. (The
-// plain W8A8 epilogue is rounded exactly; after an activation there is no
-// exact value to round to.)
+// rounding (2^-24 relative), the token scale adds one and the fused step with
+// the channel scale and the bias one more: less than 2^-22 of |acc sx sw| +
+// |bias| in all, a thousandth of the result's half step unless the bias
+// nearly cancels the product. (The plain W8A8 epilogue is rounded exactly in
+// that case too; after an activation there is no exact value to round to.)
 template <int KIND>
 __device__ __forceinline__ F2 pre_act2(uint32_t a0, uint32_t a1, float sx0, float sx1, const RowF& c) {
   if constexpr (KIND == kW8A8) {
