@@ -279,8 +279,11 @@ aria_status aria_gated_bwd_workspace_size(int64_t M, int64_t N, int64_t K, size_
  * is deterministic); dG and dU are rounded to fp16 as operands of the
  * products, the bias gradients are summed before that rounding, and each
  * output is rounded once. (How dX's sum over the channels is divided depends
- * on the sizes and on whether dWg and dWu are asked for.) dH should be scaled so that dG, dU and the outputs
- * stay within fp16's range, as fp16 training does anyway.
+ * on the sizes and on whether dWg and dWu are asked for.) dH should be scaled
+ * so that dG, dU and the outputs stay within fp16's normal range, as fp16
+ * training does anyway: an element of dG or dU is off by half a step, 2^-11
+ * of itself from 2^-14 up, 2^-25 below (where it is lost under 2^-25), and
+ * infinite above 65504.
  * Shape rules: M >= 1; N, K >= 16 and multiples of 16. Stream order: every
  * input is read, and every output written, after the preceding kernel.
  */

@@ -5,9 +5,15 @@
 //
 // from the kept pre-activations, and the column sums of both (the bias
 // gradients) from the unrounded fp32 values. dG and dU are rounded to fp16,
-// once: they are the operands of the two products that follow, and their
-// relative error of 2^-11 per element adds, independent from element to
-// element, about as much to those products as rounding their results does.
+// once: they are the operands of the two products that follow, whose other
+// operands are fp16 too. An element of at least 2^-14 is off by 2^-11 of
+// itself, independent from element to element, which adds about as much to
+// those products as rounding their results does (2.9e-4 against 2.1e-4 in
+// norm). A smaller element is off by up to 2^-25, its bits among the
+// subnormals, and one above 65504 becomes infinite: dH's scale has to keep
+// the two within that range, as it has to for dH itself, which is fp16. (A
+// scale of the kernel's own would have to be known before the first element
+// is rounded: one more pass over the three inputs.)
 //
 // Memory-bound: 6 bytes read and 4 written per element. A block covers 128
 // columns x `rows` rows, 16 threads along the columns (8 each, 16-byte
