@@ -234,7 +234,8 @@ __device__ __forceinline__ RowRaw row_raw(int n, const GemmParams& p, bool up = 
   RowRaw r;
   if (n >= p.N) return r;
   if constexpr (EPI == kEpiGated) {
-    if constexpr (KIND == kW8A8 || KIND == kQ8) r.sw = __ldg((up ? p.sw_u : p.sw) + n);
+    // (behind the wait: a call that keeps the pre-activations promises it)
+    if constexpr (KIND == kW8A8 || KIND == kQ8) r.sw = ld_dep_f32((up ? p.sw_u : p.sw) + n);
     const __half* b = up ? p.bias_u : p.bias;
     if (b) r.bias = ld_dep_u16(b + n);
     return r;

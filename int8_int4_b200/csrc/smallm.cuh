@@ -235,11 +235,12 @@ __global__ void __launch_bounds__(kSmThreads, 2) smallm_kernel(const SmallParams
     }
   }
   // q8: the channel scales of the CTA's rows (part of the pack, like the
-  // weights) into shared memory, also before the wait
+  // weights) into shared memory, also before the wait unless w_late (loads
+  // that keep their place in program order)
   float* s_sw = reinterpret_cast<float*>(sm + p.off_sw);
   if constexpr (KIND == kQ8)
     for (int r = tid; r < R; r += kSmThreads)
-      s_sw[r] = __ldg(((RPC == 2 && (r & 1)) ? p.sw_u : p.sw) + r0 + r / RPC);
+      s_sw[r] = ld_dep_f32(((RPC == 2 && (r & 1)) ? p.sw_u : p.sw) + r0 + r / RPC);
   if (tid == 0) ARIA_STAMP(1);
   pdl_launch_dependents();  // the next launch may start streaming its own weights
   pdl_wait();               // X, the epilogue operands and Y belong to the stream order

@@ -98,3 +98,23 @@ def test_packed_by_the_preceding_kernel(fmt, M):
             aq.qpack(pf, scaled[k][0], out=Pg)
             return Pg, Pu
         check(lambda g, u: aq.qgemm_gated(fmt, X, *g, *u, sx=sx, save=save), write)
+
+
+@pytest.mark.parametrize("fmt", ["q8", "q4", "w8a8"])
+@pytest.mark.parametrize("M", [1, 16, 64, 300, 1100])
+def test_packed_weights_written_by_an_ordinary_kernel(fmt, M):
+    """A call that keeps G and U: packed weights and scales that plain copies
+    right before it write, the scales last."""
+    X, sx = (normal(1, M, K), None) if fmt != "w8a8" else aq.act_quant(normal(1, M, K))
+    pf = "q4" if fmt == "q4" else "q8"
+    g0, u0 = normal(4, N, K, std=0.05), normal(5, N, K, std=0.05)
+    packs = {k: (aq.qpack(pf, g0 * k), aq.qpack(pf, u0 * k)) for k in FACTORS}
+    Pg, Pu = weight(pf, 9, N, K)[:2], weight(pf, 10, N, K)[:2]
+    G, U = (torch.empty(M, N, dtype=torch.float16, device="cuda") for _ in range(2))
+
+    def write(k):
+        for i in (0, 1):
+            for dst, src in zip((Pu[i], Pg[i]), (packs[k][1][i], packs[k][0][i])):
+                dst.copy_(src)
+        return Pg, Pu
+    check(lambda g, u: aq.qgemm_gated(fmt, X, *g, *u, sx=sx, save=(G, U)), write)
