@@ -1175,7 +1175,8 @@ aria_status out_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols
 // remaining constants are fitted to a sweep over five weight shapes and nine
 // token counts from 48 to 4096 (180 cases of either operator, the linear with
 // a residual), where the choice then costs 0.6 % over the best of the four
-// variants on average.
+// variants on average, and 0.5 % (11 % at most) on 100 cases of five weight
+// shapes outside the fit, 8192 x 2048 to 1280 x 5120.
 struct TgChoice {
   int bn = 256;
   double us = 0.0;
