@@ -577,7 +577,7 @@ def gated_backward(dH: torch.Tensor, X, Wg, Wu, G: torch.Tensor, U: torch.Tensor
     ``out``: a tuple of five tensors to write (None where nothing is asked
     for). ``workspace``: a uint8 tensor of gated_backward_workspace_size(M, N, K,
     dH.device) bytes; calls sharing one must not overlap on the GPU. X is needed for the
-    weight gradients only and the weights for dX only; K comes from either."""
+    weight gradients only and the weights for dX only; K comes from any of them."""
     if dH.dim() != 2:
         raise ValueError("dH must be 2-D")
     di = dH.get_device()

@@ -1188,7 +1188,7 @@ TgChoice choose_tg(bool gated, int64_t M, int64_t N, int64_t nkb) {
   for (int bn : {256, 192, 128}) {
     const int chans = gated ? bn / 2 : bn;
     const int64_t waves = (tr * ((N + chans - 1) / chans) + pairs - 1) / pairs;
-    const double kb = std::max(2 * bn, 256 + bn) / 1850.0;  // us per K block
+    const double kb = std::max(2 * bn, 256 + bn) / 1850.0;  // us per K block at 1850 cycles per us
     const double epi = bn / 64 * (gated ? 0.45 : 1.0);      // a tile's epilogue
     const double main = static_cast<double>(nkb) * kb;
     const double t = 2.8 + epi + static_cast<double>(waves) * (1.5 + std::max(main, epi) + 0.75 * std::min(main, epi));
@@ -1213,6 +1213,8 @@ bool use_tg(int kind, bool gated, int64_t M, int64_t N, int64_t K, int* bn) {
   const int64_t sms = dev_info().sms, ctas = static_cast<int64_t>(pl.p.tiles) * pl.p.splits;
   const double kb = 2.0 * (128 + pl.p.BN) / 1850.0, epi = pl.p.BN * 0.022;
   const double main = static_cast<double>(nkb) / pl.p.splits * kb;
+  // (6.0 for a split launch: its exchange and the epilogue behind it, fitted to
+  // fp16 and W8A8; plan_gemm's estimate of q8's and q4's exchange is another fit)
   const double chan = 0.5 + (pl.p.splits > 1 ? 6.0 : epi) +
                       static_cast<double>((ctas + sms - 1) / sms) * (std::max(main, epi) + 0.8 * std::min(main, epi));
   return tg.us < chan;
